@@ -1,5 +1,6 @@
 /*
- * moe.h -- C ABI of the MI355X (gfx950) MoE layer forward pass.
+ * moe.h -- C ABI of the MI355X (gfx950) MoE layer: the forward pass, the
+ * backward pass of its steps, and the forward pass on 8-bit expert weights.
  *
  * One MoE layer, as described on the pages this library follows:
  *   [NOTES] "MoE notes: what one token goes through in an MoE layer"
@@ -19,6 +20,10 @@
  *              that expert's rows, as a grouped GEMM.   [NOTES] §2 step 3
  *   combine  : y[t] = sum_k w[t,k] h[t,k] back in token order.
  *                                                 [NOTES] §2 step 4, §2.3
+ *   training : the experts' FFN keeping its gate and up projections, and the
+ *              gradients of the FFN, the combine and the routing.
+ *   8 bits   : the experts' FFN on int8 rows and weights with a scale for
+ *              each row and each output channel.
  *   aux/bias : aux = E sum_e f_e P_e ([NOTES] §1.2); per-expert bias +-alpha
  *              toward the average load ([ENG] §1.2).
  *
@@ -292,12 +297,126 @@ moe_status moe_router_losses(const moe_problem* p, const float* logits, const fl
                              const int32_t* topk_ids, const int32_t* counts, float* z_loss,
                              float* aux_topk, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- training ---------------------------------------------------------------
+ * The backward pass of the layer is the four steps below in reverse:
+ *   moe_combine_backward  dy -> dh, dtopk_w
+ *   moe_expert_ffn_backward  dh -> dx_perm, dw1, dw3, dw2
+ *   moe_route_backward  dtopk_w, dx_perm -> dlogits, dx, dw_router
+ * after a forward pass of moe_route, moe_dispatch (with x), moe_expert_ffn_train
+ * and moe_combine.  Every gradient is written, none is added to; sums are fp32
+ * in a fixed order (run-to-run identical) and rounded once to the output's
+ * type.  Outputs overlap no input and no other output. */
+
+/* moe_expert_ffn that keeps what its backward pass reads.  Arguments as there,
+ * with
+ *   gate, up [T*K, F] dtype out: x_perm W1_e^T and x_perm W3_e^T, rounded to
+ *            dtype (h is computed from the unrounded ones)
+ *   h        [T*K, d] dtype out
+ * Rows >= offsets[E] of gate, up and h are left untouched. */
+moe_status moe_expert_ffn_train_workspace_size(const moe_problem* p, size_t* bytes);
+moe_status moe_expert_ffn_train(const moe_problem* p, const void* x_perm, const int32_t* offsets,
+                                const void* w1, const void* w3, const void* w2, void* gate, void* up,
+                                void* h, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of the expert FFN.  With s = sigmoid(gate), act = gate s up and
+ * dact = dh W2_e:
+ *   dgate = dact up s (1 + gate (1 - s)),  dup = dact gate s
+ *   dx_perm [T*K, d]  = dgate W1_e + dup W3_e        (NULL: not computed)
+ *   dw1 [E, F, d] = dgate^T x_perm,  dw3 [E, F, d] = dup^T x_perm,
+ *   dw2 [E, d, F] = dh^T act, each over the rows of its expert
+ *                                     (all three NULL: not computed)
+ *   dh [T*K, d]; dact stays fp32, dgate, dup and act are rounded to dtype
+ * An expert without rows gets zero weight gradients.  Rows >= offsets[E] of
+ * the inputs are not used and those of dx_perm left untouched. */
+moe_status moe_expert_ffn_backward_workspace_size(const moe_problem* p, size_t* bytes);
+moe_status moe_expert_ffn_backward(const moe_problem* p, const void* x_perm, const int32_t* offsets,
+                                   const void* w1, const void* w3, const void* w2, const void* gate,
+                                   const void* up, const void* dh, void* dx_perm, void* dw1, void* dw3,
+                                   void* dw2, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of the weighted combine.
+ *   dy [T, d] dtype, h [T*K, d] dtype (grouped rows), assign_row [T*K],
+ *   topk_w [T, K] fp32
+ *   dh      [T*K, d] dtype out: dh[assign_row[t,k]] = topk_w[t,k] dy[t]; rows
+ *           that no slot owns are left untouched
+ *   dtopk_w [T, K] fp32 out: <dy[t], h[assign_row[t,k]]>, 0 for a dropped
+ *           slot; h and dtopk_w may be NULL together */
+moe_status moe_combine_backward(const moe_problem* p, const void* dy, const void* h, const int32_t* assign_row,
+                                const float* topk_w, void* dh, float* dtopk_w, void* stream);
+
+/* Gradients of routing and of the dispatch's row gather.
+ *   x [T, d], w_router [d, E] dtype; logit_bias [E] or NULL; logits [T, E],
+ *   topk_ids, topk_w [T, K] as moe_route wrote them
+ *   dtopk_w [T, K] fp32, or NULL for none (as under MOE_FLAG_COMBINE_MEAN,
+ *           where it is ignored)
+ *   counts  [E] (required when d_aux != 0), d_aux: gradient of the loss with
+ *           respect to the aux loss of moe_aux_loss, its f_e taken as constant
+ *   d_z     gradient with respect to the z-loss of moe_router_losses
+ *   dlogits [T, E] fp32 out: of the scores
+ *   dx_perm [T*K, d] dtype and assign_row [T*K], or both NULL
+ *   dx      [T, d] dtype out, or NULL: sum over k ascending of
+ *           dx_perm[assign_row[t,k]] (dropped slots add nothing) plus
+ *           dlogits W_r^T
+ *   dw_router [d, E] dtype out, or NULL: x^T dlogits
+ *   ws      moe_route_backward_workspace_size bytes (may be NULL when
+ *           dw_router is) */
+moe_status moe_route_backward_workspace_size(const moe_problem* p, size_t* bytes);
+moe_status moe_route_backward(const moe_problem* p, const void* x, const void* w_router, const float* logit_bias,
+                              const float* logits, const int32_t* topk_ids, const float* topk_w,
+                              const float* dtopk_w, const int32_t* counts, float d_aux, float d_z,
+                              const void* dx_perm, const int32_t* assign_row, float* dlogits, void* dx,
+                              void* dw_router, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- 8-bit expert FFN ----------------------------------------------------------
+ * Symmetric quantisation of each row of x [rows, cols] (dtype fp32 or bf16,
+ * cols a multiple of 8, <= 65536):
+ *   scale[r] = max(max_c |x[r,c]| / 127, 2^-126) in fp32
+ *   q[r,c]   = x[r,c] / scale[r] rounded to the nearest integer, ties to even
+ * A row that holds an infinity or a NaN gets a NaN scale and zeros.  Weights
+ * are quantised with it once, a row per output channel: w1, w3 as [E*F, d],
+ * w2 as [E*d, F]. */
+moe_status moe_quantize_rows(int64_t rows, int32_t cols, int32_t dtype, const void* x, int8_t* q, float* scale,
+                             void* stream);
+
+/* The experts' weights in 8 bits with a scale for each output channel. */
+typedef struct {
+    const int8_t* w1; /* [E, F, d] */
+    const int8_t* w3; /* [E, F, d] */
+    const int8_t* w2; /* [E, d, F] */
+    const float* s1;  /* [E, F] */
+    const float* s3;  /* [E, F] */
+    const float* s2;  /* [E, d] */
+} moe_i8_weights;
+
+/* moe_expert_ffn on 8-bit weights (dtype bf16; d and F multiples of 16, else
+ * MOE_ERR_UNSUPPORTED).  Each row of x_perm is quantised as above, and so is
+ * each row of act; the products are exact integer sums:
+ *   g = (sum_k x_q w1_q) scale s1,  u = (sum_k x_q w3_q) scale s3
+ *   act [T*K, F] out: SiLU(g) u, rounded to bf16
+ *   h   [T*K, d] out: (sum_f act_q w2_q) scale s2, rounded to bf16
+ * Rows >= offsets[E] of act and h are left untouched. */
+moe_status moe_expert_ffn_i8_workspace_size(const moe_problem* p, size_t* bytes);
+moe_status moe_expert_ffn_i8(const moe_problem* p, const void* x_perm, const int32_t* offsets,
+                             const moe_i8_weights* w, void* act, void* h, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* moe_forward on 8-bit expert weights: routing, dispatch and combine as there
+ * (in bf16 and fp32), the experts as moe_expert_ffn_i8.  Each token's row is
+ * quantised once. */
+moe_status moe_forward_i8_workspace_size(const moe_problem* p, size_t* bytes);
+moe_status moe_forward_i8(const moe_problem* p, const void* x, const void* w_router, const moe_i8_weights* w,
+                          const float* logit_bias, void* y, const moe_debug_out* dbg, void* ws,
+                          size_t ws_bytes, void* stream);
+
 /* ---- timing hook (tracing, not part of the layer) -------------------------
  * Kernels of the library, by id, for moe_set_kernel_timer / moe_kernel_name.
  * MOE_KERNEL_FFN times the whole expert FFN (both GEMMs, every launch).
  * MOE_KERNEL_FFN_GATE_UP and MOE_KERNEL_FFN_DOWN time one GEMM step each,
  * with every launch it takes (on large batches, the tiled GEMM, the
- * small-expert launch and the k-split launches of the second GEMM). */
+ * small-expert launch and the k-split launches of the second GEMM).
+ * MOE_KERNEL_FFN_TRAIN, _FFN_BACKWARD, _COMBINE_BACKWARD, _ROUTE_BACKWARD and
+ * _FFN_I8 time the whole call of that name, MOE_KERNEL_QUANTIZE each
+ * quantisation (those inside the 8-bit FFN too). */
 enum {
     MOE_KERNEL_ROUTER = 0,
     MOE_KERNEL_DISPATCH_COUNT = 1,
@@ -312,7 +431,13 @@ enum {
     MOE_KERNEL_FFN_PLAN = 10,
     MOE_KERNEL_ROUTER_LOSSES = 11,
     MOE_KERNEL_FFN = 12,
-    MOE_KERNEL_COUNT = 13
+    MOE_KERNEL_FFN_TRAIN = 13,
+    MOE_KERNEL_FFN_BACKWARD = 14,
+    MOE_KERNEL_COMBINE_BACKWARD = 15,
+    MOE_KERNEL_ROUTE_BACKWARD = 16,
+    MOE_KERNEL_QUANTIZE = 17,
+    MOE_KERNEL_FFN_I8 = 18,
+    MOE_KERNEL_COUNT = 19
 };
 
 /* Name of kernel `kid` ("?" when out of range). */

@@ -1,0 +1,129 @@
+// Grouped gated FFN on 8-bit integers.  Rows a (quantised per row to a_q, s_a)
+// against weights quantised per output channel (w_q, s_w):
+//   g = (sum_k a_q w1_q) s_a s1,  u likewise,  act = bf16(silu(g) u),
+//   h = (sum_f act_q w2_q) s_act s2
+// The integer sums are exact in 32 bits (at most 65536 * 127 * 127 < 2^31),
+// so their order does not matter; scales and the gate are fp32.
+#include "../device_common.h"
+#include "../launch.h"
+#include "ffn_tiles.h"
+
+namespace moe {
+
+namespace {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int I8_ALIGN = 128;  // the quantised rows are padded with zeros to whole 128-byte lines
+constexpr int I8_BM = 128;     // rows per row tile
+
+// One wave: 16 weight rows against up to 128 rows of a group, 64 k per step;
+// lane l feeds row l % 16 and k (l / 16) * 16 .. + 15 of both operands.
+template <bool GATED>
+__global__ __launch_bounds__(256) void ffn_i8_kernel(int n_rows, int N, int K, int lda, const int8_t* __restrict__ A,
+                                                    const float* __restrict__ sa, const int32_t* __restrict__ rowmap,
+                                                    int topk, RowPlan plan, const int32_t* __restrict__ offsets,
+                                                    const int8_t* __restrict__ wa, const float* __restrict__ swa,
+                                                    const int8_t* __restrict__ wb, const float* __restrict__ swb,
+                                                    bf16* __restrict__ out) {
+    constexpr int NG = GATED ? 2 : 1, NB = I8_BM / 16;
+    if ((int)blockIdx.x >= *plan.mt_count) return;
+    const int e = plan.mt_expert[blockIdx.x] & 0x7FF;
+    const int row0 = plan.mt_row0[blockIdx.x];
+    const int row_end = min(offsets[e + 1], n_rows);
+    const int lane = lane_id();
+    const int n0 = blockIdx.y * 64 + (threadIdx.x / kWave) * 16;
+    if (n0 >= N) return;
+    const int rl = lane & 15, kg = (lane >> 4) * 16;
+    const size_t wrow = (size_t)e * N + n0 + rl;  // N is a multiple of 16
+    const int8_t* pw[2] = {wa + wrow * K, GATED ? wb + wrow * K : nullptr};
+    const int8_t* pa[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        pa[b] = A + (size_t)src_row(rowmap, topk, min(row0 + 16 * b + rl, row_end - 1)) * lda;
+    i32x4 acc[NG][NB];
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[i][b] = i32x4{0, 0, 0, 0};
+    for (int k = kg; k < lda; k += 64) {
+        i32x4 w[NG];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const i32x4 zero = {0, 0, 0, 0};
+            w[i] = k < K ? *reinterpret_cast<const i32x4*>(pw[i] + k) : zero;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const i32x4 a = *reinterpret_cast<const i32x4*>(pa[b] + k);
+#pragma unroll
+            for (int i = 0; i < NG; ++i) acc[i][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], a, acc[i][b], 0, 0, 0);
+        }
+    }
+    // element i of a block: weight row n0 + 4 (lane / 16) + i, grouped row lane % 16
+    const int n = n0 + 4 * (lane >> 4);
+    const f32x4 s1 = *reinterpret_cast<const f32x4*>(swa + (size_t)e * N + n);
+    f32x4 s3 = {0, 0, 0, 0};
+    if (GATED) s3 = *reinterpret_cast<const f32x4*>(swb + (size_t)e * N + n);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int r = row0 + 16 * b + rl;
+        if (r >= row_end) continue;
+        const float s = sa[src_row(rowmap, topk, r)];
+        bf16x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float g = (float)acc[0][b][i] * s * s1[i];
+            if constexpr (GATED) v[i] = (bf16)(silu(g) * ((float)acc[1][b][i] * s * s3[i]));
+            else v[i] = (bf16)g;
+        }
+        *reinterpret_cast<bf16x4*>(out + (size_t)r * N + n) = v;
+    }
+}
+
+struct I8Layout {
+    int ldx, ldf;
+    size_t xq, xs, aq, as, plan, total;
+};
+I8Layout i8_layout(int n_x, int n, int E, int d, int F) {
+    I8Layout L;
+    L.ldx = (int)align_up(d, I8_ALIGN);
+    L.ldf = (int)align_up(F, I8_ALIGN);
+    L.xq = 0;
+    L.xs = L.xq + align_up((size_t)n_x * L.ldx, 256);
+    L.aq = L.xs + align_up((size_t)n_x * sizeof(float), 256);
+    L.as = L.aq + align_up((size_t)n * L.ldf, 256);
+    L.plan = L.as + align_up((size_t)n * sizeof(float), 256);
+    L.total = L.plan + row_plan_bytes(n, E);
+    return L;
+}
+
+}  // namespace
+
+size_t ffn_i8_ws_bytes(int n_x, int n_rows, int E, int d, int F) { return i8_layout(n_x, n_rows, E, d, F).total; }
+
+hipError_t launch_ffn_i8(int n_x, int n, int K, int E, int d, int F, const void* x, const int32_t* rowmap,
+                         const int32_t* offsets, const moe_i8_weights& w, void* act, void* h, void* ws, hipStream_t s) {
+    const I8Layout L = i8_layout(n_x, n, E, d, F);
+    char* base = (char*)ws;
+    int8_t *xq = (int8_t*)base + L.xq, *aq = (int8_t*)base + L.aq;
+    float *xs = (float*)(base + L.xs), *as = (float*)(base + L.as);
+    timer_before(MOE_KERNEL_FFN_I8, s);
+    // grouped rows past the last group are not read; token rows all are
+    hipError_t err = launch_quantize_rows(n_x, d, L.ldx, MOE_DTYPE_BF16, x, xq, xs, rowmap ? nullptr : offsets + E, s);
+    if (err != hipSuccess) return err;
+    RowPlan plan;
+    if ((err = launch_row_plan(n, E, I8_BM, offsets, base + L.plan, &plan, s)) != hipSuccess) return err;
+    const unsigned mt = (unsigned)row_plan_tiles(n, E, I8_BM);
+    ffn_i8_kernel<true><<<dim3(mt, (F + 63) / 64), 256, 0, s>>>(n, F, d, L.ldx, xq, xs, rowmap, K, plan, offsets, w.w1,
+                                                               w.s1, w.w3, w.s3, (bf16*)act);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    if ((err = launch_quantize_rows(n, F, L.ldf, MOE_DTYPE_BF16, act, aq, as, offsets + E, s)) != hipSuccess) return err;
+    ffn_i8_kernel<false><<<dim3(mt, (d + 63) / 64), 256, 0, s>>>(n, d, F, L.ldf, aq, as, nullptr, 1, plan, offsets,
+                                                                w.w2, w.s2, nullptr, nullptr, (bf16*)h);
+    err = hipGetLastError();
+    if (err == hipSuccess) timer_after(MOE_KERNEL_FFN_I8, s);
+    return err;
+}
+
+}  // namespace moe

@@ -77,4 +77,14 @@ __device__ __forceinline__ PfTile pf_tile(int t, int n_mt, int n_nt, const int32
 // of at least 128 rows, one partial tile per expert).
 int prefill_max_mtiles(int n_rows, int E);
 
+// Row tiles of every expert's group, bm rows each (an expert's last one partly
+// filled), in device memory: *mt_count tiles, packed as ffn_plan_kernel says.
+struct RowPlan {
+    const int32_t *mt_count = nullptr, *mt_expert = nullptr, *mt_row0 = nullptr;
+};
+// Most row tiles there can be (the plan's grid bound).
+inline int row_plan_tiles(int n_rows, int E, int bm) { return n_rows / bm + E + 1; }
+size_t row_plan_bytes(int n_rows, int E);
+hipError_t launch_row_plan(int n_rows, int E, int bm, const int32_t* offsets, void* ws, RowPlan* plan, hipStream_t s);
+
 }  // namespace moe

@@ -1,0 +1,170 @@
+// The grouped gated FFN in training: the forward pass that keeps the gate and
+// up projections, and the backward pass.  With the rows a of expert e
+//   g = W1 a,  u = W3 a,  act = silu(g) u,  h = W2 act
+//   da = W2^T dh;  dg, du from da, g, u (gated.h)
+//   dx = W1^T dg + W3^T du;  dW1 = sum dg a^T;  dW3 = sum du a^T;  dW2 = sum dh act^T
+// g and u are stored in the layer type; act is formed again from them in the
+// backward pass (two stored rows of F instead of three).
+#include "../device_common.h"
+#include "../launch.h"
+#include "ffn_tiles.h"
+#include "gated.h"
+#include "gemm_f32.h"
+
+namespace moe {
+
+namespace {
+
+// ---- fp32 path -------------------------------------------------------------------
+template <typename T>
+struct EpiGate {
+    T *gate, *up, *act;
+    __device__ void operator()(int, int, int m, int n, int N, const f32x4 (&v)[2]) const {
+        const size_t i = (size_t)m * N + n;
+        store_f32x4(gate + i, v[0]);
+        store_f32x4(up + i, v[1]);
+        f32x4 a;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = silu(v[0][j]) * v[1][j];
+        store_f32x4(act + i, a);
+    }
+};
+template <typename T>
+struct EpiRows {  // C rows are grouped rows
+    T* out;
+    __device__ void operator()(int, int, int m, int n, int N, const f32x4 (&v)[2]) const {
+        store_f32x4(out + (size_t)m * N + n, v[0]);
+    }
+};
+template <typename T>
+struct EpiGateGrad {
+    const T *gate, *up;
+    T *dgate, *dup, *act;
+    __device__ void operator()(int, int, int m, int n, int N, const f32x4 (&v)[2]) const {
+        const size_t i = (size_t)m * N + n;
+        const f32x4 g = load_f32x4(gate + i), u = load_f32x4(up + i);
+        f32x4 dg, du, a;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const GatedGrad r = gated_grad(g[j], u[j], v[0][j]);
+            dg[j] = r.dg;
+            du[j] = r.du;
+            a[j] = r.act;
+        }
+        store_f32x4(dgate + i, dg);
+        store_f32x4(dup + i, du);
+        store_f32x4(act + i, a);
+    }
+};
+template <typename T>
+struct EpiWeights {  // C is one expert's [M][N]
+    T *out0, *out1;
+    int M;
+    __device__ void operator()(int e, int sel, int m, int n, int N, const f32x4 (&v)[2]) const {
+        store_f32x4((sel ? out1 : out0) + ((size_t)e * M + m) * N + n, v[0]);
+    }
+};
+
+template <typename T>
+hipError_t train_gemms(int n, int E, int d, int F, const T* x, const int32_t* offsets, const T* w1, const T* w3,
+                       const T* w2, T* gate, T* up, T* act, T* h, const RowPlan& plan, hipStream_t s) {
+    const unsigned mt = (unsigned)row_plan_tiles(n, E, GM_T);
+    GemmArgs<T, T> g{{x, nullptr}, {w1, w3}, d, d, (size_t)F * d, 0, F, d, n, E, plan, offsets};
+    gemm_f32_kernel<GM_NT, true, 1, true, true><<<dim3(mt, (F + GM_T - 1) / GM_T), 256, 0, s>>>(
+        g, EpiGate<T>{gate, up, act});
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    GemmArgs<T, T> g2{{act, nullptr}, {w2, nullptr}, F, F, (size_t)F * d, 0, d, F, n, E, plan, offsets};
+    gemm_f32_kernel<GM_NT, false, 1, true, true><<<dim3(mt, (d + GM_T - 1) / GM_T), 256, 0, s>>>(g2, EpiRows<T>{h});
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t backward_gemms(int n, int E, int d, int F, const T* x, const int32_t* offsets, const T* w1, const T* w3,
+                          const T* w2, const T* gate, const T* up, const T* dh, T* dx, T* dw1, T* dw3, T* dw2,
+                          T* dgate, T* dup, T* act, const RowPlan& plan, hipStream_t s) {
+    const unsigned mt = (unsigned)row_plan_tiles(n, E, GM_T);
+    const unsigned td = (d + GM_T - 1) / GM_T, tf = (F + GM_T - 1) / GM_T;
+    const size_t ws = (size_t)F * d;
+    GemmArgs<T, T> ga{{dh, nullptr}, {w2, nullptr}, d, F, ws, 0, F, d, n, E, plan, offsets};
+    gemm_f32_kernel<GM_NN, false, 1, true, true><<<dim3(mt, tf), 256, 0, s>>>(
+        ga, EpiGateGrad<T>{gate, up, dgate, dup, act});
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    if (dw2 != nullptr) {
+        GemmArgs<T, T> g{{dh, nullptr}, {act, nullptr}, d, F, 0, d, F, 0, n, E, RowPlan{}, offsets};
+        gemm_f32_kernel<GM_TN, false, 1, true, true><<<dim3(tf, td, E), 256, 0, s>>>(g, EpiWeights<T>{dw2, nullptr, d});
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+        GemmArgs<T, T> g13{{dgate, dup}, {x, nullptr}, F, d, 0, F, d, 0, n, E, RowPlan{}, offsets};
+        gemm_f32_kernel<GM_TN, false, 1, true, true><<<dim3(td, tf, 2 * E), 256, 0, s>>>(g13,
+                                                                                        EpiWeights<T>{dw1, dw3, F});
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
+    if (dx != nullptr) {
+        GemmArgs<T, T> g{{dgate, dup}, {w1, w3}, F, d, ws, 0, d, F, n, E, plan, offsets};
+        gemm_f32_kernel<GM_NN, false, 2, true, true><<<dim3(mt, td), 256, 0, s>>>(g, EpiRows<T>{dx});
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+// act, then the row plan
+size_t ffn_train_ws_bytes(int T, int K, int E, int d, int F, int dtype) {
+    const size_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
+    return align_up((size_t)T * K * F * es, 256) + row_plan_bytes(T * K, E);
+}
+
+hipError_t launch_ffn_train(int T, int K, int E, int d, int F, int dtype, const void* x, const int32_t* offsets,
+                            const void* w1, const void* w3, const void* w2, void* gate, void* up, void* h, void* ws,
+                            hipStream_t s) {
+    const int n = T * K;
+    const size_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
+    char* base = (char*)ws;
+    RowPlan plan;
+    timer_before(MOE_KERNEL_FFN_TRAIN, s);
+    hipError_t err = launch_row_plan(n, E, GM_T, offsets, base + align_up((size_t)n * F * es, 256), &plan, s);
+    if (err != hipSuccess) return err;
+    if (dtype == MOE_DTYPE_F32)
+        err = train_gemms<float>(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3,
+                                  (const float*)w2, (float*)gate, (float*)up, (float*)base, (float*)h, plan, s);
+    else
+        err = train_gemms<bf16>(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3,
+                                (const bf16*)w2, (bf16*)gate, (bf16*)up, (bf16*)base, (bf16*)h, plan, s);
+    if (err == hipSuccess) timer_after(MOE_KERNEL_FFN_TRAIN, s);
+    return err;
+}
+
+// dgate, dup, act, then the row plan
+size_t ffn_backward_ws_bytes(int T, int K, int E, int d, int F, int dtype) {
+    const size_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
+    return 3 * align_up((size_t)T * K * F * es, 256) + row_plan_bytes(T * K, E);
+}
+
+hipError_t launch_ffn_backward(int T, int K, int E, int d, int F, int dtype, const void* x, const int32_t* offsets,
+                               const void* w1, const void* w3, const void* w2, const void* gate, const void* up,
+                               const void* dh, void* dx, void* dw1, void* dw3, void* dw2, void* ws, hipStream_t s) {
+    const int n = T * K;
+    const size_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
+    const size_t one = align_up((size_t)n * F * es, 256);
+    char* base = (char*)ws;
+    RowPlan plan;
+    timer_before(MOE_KERNEL_FFN_BACKWARD, s);
+    hipError_t err = launch_row_plan(n, E, GM_T, offsets, base + 3 * one, &plan, s);
+    if (err != hipSuccess) return err;
+    if (dtype == MOE_DTYPE_F32)
+        err = backward_gemms<float>(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3,
+                                     (const float*)w2, (const float*)gate, (const float*)up, (const float*)dh,
+                                     (float*)dx, (float*)dw1, (float*)dw3, (float*)dw2, (float*)base,
+                                     (float*)(base + one), (float*)(base + 2 * one), plan, s);
+    else
+        err = backward_gemms<bf16>(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3,
+                                   (const bf16*)w2, (const bf16*)gate, (const bf16*)up, (const bf16*)dh, (bf16*)dx,
+                                   (bf16*)dw1, (bf16*)dw3, (bf16*)dw2, (bf16*)base, (bf16*)(base + one),
+                                   (bf16*)(base + 2 * one), plan, s);
+    if (err == hipSuccess) timer_after(MOE_KERNEL_FFN_BACKWARD, s);
+    return err;
+}
+
+}  // namespace moe

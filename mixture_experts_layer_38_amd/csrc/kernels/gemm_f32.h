@@ -1,0 +1,222 @@
+// Grouped matrix products in fp32: 128 x 128 output tiles on the fp32 MFMA
+// (v_mfma_f32_32x32x2_f32, exact products, fp32 sums in a fixed order), for
+// the fp32 layer and for operands that must not be rounded to bf16.  bf16
+// operands are widened on the way into the LDS.
+//
+//   GM_NT  C[r][n] = sum_k A[r][k] B[n][k]     rows r of one expert's group
+//   GM_NN  C[r][n] = sum_k A[r][k] B[k][n]
+//   GM_TN  C[m][n] = sum_r A[r][m] B[r][n]     the sum runs over the group's rows
+//
+// A workgroup of four waves owns a tile; wave (wm, wn) owns 64 x 64 of it.
+// Operands go through registers (the next 16-wide k step is loaded while the
+// present one is multiplied) into LDS tiles [k][row], padded so that the
+// column reads of the MFMA operands and the transposing writes fall in
+// distinct banks.
+#pragma once
+
+#include "../device_common.h"
+#include "ffn_tiles.h"
+
+namespace moe {
+
+constexpr int GM_T = 128;        // tile rows and columns
+constexpr int GM_K = 16;         // k per step
+constexpr int GM_LD = GM_T + 4;  // padded LDS row (floats)
+enum { GM_NT, GM_NN, GM_TN };
+
+// One product of every group.  a[1], b[1]: the second factor pair where the
+// kernel takes two (DUAL: two products of the same rows; SEGS = 2: the sum of
+// two products; GM_TN: the second half of the grid's z takes a[1]).
+template <typename TA, typename TB>
+struct GemmArgs {
+    const TA* a[2];
+    const TB* b[2];
+    int lda, ldb;
+    size_t b_stride;  // elements from one expert's B to the next's (GM_NT, GM_NN)
+    int M, N, K;      // GM_TN: C is [M][N]; else K is the reduction length
+    int n_rows;       // grouped rows
+    int E;            // experts (GM_TN: the grid's z counts them, once or twice)
+    RowPlan plan;     // row tiles of the groups (mt_count NULL: one group of n_rows rows)
+    const int32_t* offsets;  // NULL: one group; GM_TN then cuts its rows into gridDim.z parts
+};
+
+// Eight consecutive elements of a row as floats; zeros past `left` elements.
+template <typename T, bool VEC>
+__device__ __forceinline__ void gm_load8(float (&r)[8], const T* p, int left) {
+    if (VEC) {  // left is at most 0 or at least 8
+        if (left > 0) {
+            if constexpr (sizeof(T) == 4) {
+                const f32x4 u = *reinterpret_cast<const f32x4*>(p);
+                const f32x4 v = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    r[j] = u[j];
+                    r[4 + j] = v[j];
+                }
+            } else {
+                const bf16x8 u = *reinterpret_cast<const bf16x8*>(p);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[j] = (float)u[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = j < left ? to_f32(p[j]) : 0.0f;
+    }
+}
+
+// VA, VB: rows of A (B) are whole 8-element vectors.  Epi: called as
+// epi(e, sel, m, n, N, v) for four consecutive columns n .. n + 3 of row m
+// (grouped row, or A's column for GM_TN) with the sums v[0] (and v[1] of the
+// second product).
+template <int LAYOUT, bool DUAL, int SEGS, bool VA, bool VB, typename TA, typename TB, typename Epi>
+__global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi epi) {
+    constexpr int NB = DUAL ? 2 : 1;
+    __shared__ __align__(16) float sA[GM_K][GM_LD];
+    __shared__ __align__(16) float sB[NB][GM_K][GM_LD];
+    const int tid = threadIdx.x;
+    const int lane = lane_id();
+    const int wave = tid / kWave;
+    // row tiles lie along x, which alone may pass 65535
+    const int n0 = (LAYOUT == GM_TN ? blockIdx.x : blockIdx.y) * GM_T;
+    int e = 0, sel = 0, m0, m_end, k_beg = 0, k_end = g.K;
+    if constexpr (LAYOUT == GM_TN) {
+        m0 = blockIdx.y * GM_T;
+        m_end = g.M;
+        if (g.offsets != nullptr) {
+            e = blockIdx.z % g.E;
+            sel = blockIdx.z / g.E;
+            k_beg = min(max(g.offsets[e], 0), g.n_rows);
+            k_end = min(g.offsets[e + 1], g.n_rows);
+        } else {
+            e = blockIdx.z;
+            k_beg = (int)((long long)g.n_rows * e / gridDim.z);
+            k_end = (int)((long long)g.n_rows * (e + 1) / gridDim.z);
+        }
+    } else if (g.plan.mt_count != nullptr) {
+        if ((int)blockIdx.x >= *g.plan.mt_count) return;
+        e = g.plan.mt_expert[blockIdx.x] & 0x7FF;
+        m0 = g.plan.mt_row0[blockIdx.x];
+        m_end = min(g.offsets[e + 1], g.n_rows);
+    } else {
+        m0 = blockIdx.x * GM_T;
+        m_end = g.n_rows;
+    }
+
+    const int kr = tid >> 1, kc = (tid & 1) * 8;    // a [rows][k] tile: row, first k of this thread
+    const int sr = tid >> 4, sc = (tid & 15) * 8;   // a [k][columns] tile: k, first column
+    float ra[8], rb[NB][8];
+    auto load = [&](int seg, int k0) {
+        const TA* A = g.a[LAYOUT == GM_TN ? sel : seg];
+        if constexpr (LAYOUT == GM_TN) {
+            const int r = k0 + sr;
+            gm_load8<TA, VA>(ra, A + (size_t)r * g.lda + m0 + sc, r < k_end ? g.M - m0 - sc : 0);
+        } else {
+            const int r = m0 + kr;
+            gm_load8<TA, VA>(ra, A + (size_t)r * g.lda + k0 + kc, r < m_end ? k_end - k0 - kc : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const TB* B = g.b[DUAL ? i : (LAYOUT == GM_TN ? 0 : seg)];
+            if constexpr (LAYOUT == GM_NT) {
+                const int r = n0 + kr;
+                gm_load8<TB, VB>(rb[i], B + e * g.b_stride + (size_t)r * g.ldb + k0 + kc,
+                                 r < g.N ? k_end - k0 - kc : 0);
+            } else {
+                const int r = k0 + sr;
+                gm_load8<TB, VB>(rb[i],
+                                 B + (LAYOUT == GM_TN ? 0 : e * g.b_stride) + (size_t)r * g.ldb + n0 + sc,
+                                 r < k_end ? g.N - n0 - sc : 0);
+            }
+        }
+    };
+    auto store_rows = [&](float (&s)[GM_K][GM_LD], const float (&r)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[kc + j][kr] = r[j];
+    };
+    auto store_cols = [&](float (&s)[GM_K][GM_LD], const float (&r)[8]) {
+        *reinterpret_cast<f32x4*>(&s[sr][sc]) = f32x4{r[0], r[1], r[2], r[3]};
+        *reinterpret_cast<f32x4*>(&s[sr][sc + 4]) = f32x4{r[4], r[5], r[6], r[7]};
+    };
+
+    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+    const int fr = lane & 31, fk = lane >> 5;
+    f32x16 acc[NB][2][2];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) acc[i][a][b][q] = 0.0f;
+
+    const int per = (k_end - k_beg + GM_K - 1) / GM_K;  // steps of one segment
+    const int steps = per * SEGS;
+    if (steps > 0) load(0, k_beg);
+    for (int st = 0; st < steps; ++st) {
+        __syncthreads();
+        if constexpr (LAYOUT == GM_TN) store_cols(sA, ra);
+        else store_rows(sA, ra);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            if constexpr (LAYOUT == GM_NT) store_rows(sB[i], rb[i]);
+            else store_cols(sB[i], rb[i]);
+        }
+        __syncthreads();
+        if (st + 1 < steps) {
+            const int seg = SEGS > 1 && st + 1 >= per ? 1 : 0;
+            load(seg, k_beg + (st + 1 - seg * per) * GM_K);
+        }
+#pragma unroll
+        for (int k = 0; k < GM_K; k += 2) {
+            const float a0 = sA[k + fk][wm + fr], a1 = sA[k + fk][wm + 32 + fr];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const float b0 = sB[i][k + fk][wn + fr], b1 = sB[i][k + fk][wn + 32 + fr];
+                acc[i][0][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a0, acc[i][0][0], 0, 0, 0);
+                acc[i][0][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a1, acc[i][0][1], 0, 0, 0);
+                acc[i][1][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a0, acc[i][1][0], 0, 0, 0);
+                acc[i][1][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a1, acc[i][1][1], 0, 0, 0);
+            }
+        }
+    }
+    // element i of block (nb, mb): column 8 (i / 4) + 4 (lane / 32) + i % 4, row lane % 32
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb) {
+        const int m = m0 + wm + mb * 32 + fr;
+        if (m >= m_end) continue;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = n0 + wn + nb * 32 + 8 * q + 4 * fk;
+                f32x4 v[2];
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    v[i] = f32x4{acc[i][nb][mb][4 * q], acc[i][nb][mb][4 * q + 1], acc[i][nb][mb][4 * q + 2],
+                                 acc[i][nb][mb][4 * q + 3]};
+                if (n < g.N) epi(e, sel, m, n, g.N, v);
+            }
+    }
+}
+
+// Four consecutive elements of a row (16-byte fp32 or 8-byte bf16 accesses).
+template <typename T> struct Vec4;
+template <> struct Vec4<float> { typedef f32x4 type; };
+template <> struct Vec4<bf16> { typedef bf16x4 type; };
+template <typename T>
+__device__ __forceinline__ f32x4 load_f32x4(const T* p) {
+    const typename Vec4<T>::type v = *reinterpret_cast<const typename Vec4<T>::type*>(p);
+    return f32x4{to_f32(v[0]), to_f32(v[1]), to_f32(v[2]), to_f32(v[3])};
+}
+template <typename T>
+__device__ __forceinline__ void store_f32x4(T* p, f32x4 v) {
+    *reinterpret_cast<typename Vec4<T>::type*>(p) =
+        typename Vec4<T>::type{from_f32<T>(v[0]), from_f32<T>(v[1]), from_f32<T>(v[2]), from_f32<T>(v[3])};
+}
+
+}  // namespace moe

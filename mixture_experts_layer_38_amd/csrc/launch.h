@@ -122,4 +122,34 @@ hipError_t launch_aux(int T, int K, int E, const int32_t* counts, const float* p
 hipError_t launch_bias_update(int T, int K, int E, const int32_t* counts, float alpha,
                               float* bias, hipStream_t s);
 
+// ---- training ----------------------------------------------------------------
+size_t ffn_train_ws_bytes(int T, int K, int E, int d, int F, int dtype);
+hipError_t launch_ffn_train(int T, int K, int E, int d, int F, int dtype, const void* x, const int32_t* offsets,
+                            const void* w1, const void* w3, const void* w2, void* gate, void* up, void* h, void* ws,
+                            hipStream_t s);
+// dx may be NULL; dw1, dw3 and dw2 may be NULL together.
+size_t ffn_backward_ws_bytes(int T, int K, int E, int d, int F, int dtype);
+hipError_t launch_ffn_backward(int T, int K, int E, int d, int F, int dtype, const void* x, const int32_t* offsets,
+                               const void* w1, const void* w3, const void* w2, const void* gate, const void* up,
+                               const void* dh, void* dx, void* dw1, void* dw3, void* dw2, void* ws, hipStream_t s);
+// h and dw may be NULL together.
+hipError_t launch_combine_backward(int T, int K, int d, int dtype, const void* dy, const void* h,
+                                   const int32_t* assign_row, const float* w, void* dh, float* dw, hipStream_t s);
+// dw, dx_perm, dx and dwr may be NULL (with the arguments that only they need).
+size_t route_backward_ws_bytes(int T, int d, int E);
+hipError_t launch_route_backward(int T, int d, int E, int K, int dtype, int flags, const void* x, const void* wr,
+                                 const float* bias, const float* logits, const int32_t* ids, const float* w,
+                                 const float* dw, const int32_t* counts, float d_aux, float d_z, const void* dx_perm,
+                                 const int32_t* assign_row, float* dl, void* dx, void* dwr, void* ws, hipStream_t s);
+// ---- 8-bit expert FFN ----------------------------------------------------------
+// Rows of q are ldq bytes long, zeros past cols; rows at or past *live (device
+// memory; NULL: none) are left alone.
+hipError_t launch_quantize_rows(int64_t rows, int cols, int ldq, int dtype, const void* x, int8_t* q, float* scale,
+                                const int32_t* live, hipStream_t s);
+// n_x rows of x: the n grouped rows (rowmap NULL), or the tokens that grouped
+// row r reads as rowmap[r] / K.
+size_t ffn_i8_ws_bytes(int n_x, int n_rows, int E, int d, int F);
+hipError_t launch_ffn_i8(int n_x, int n_rows, int K, int E, int d, int F, const void* x, const int32_t* rowmap,
+                         const int32_t* offsets, const moe_i8_weights& w, void* act, void* h, void* ws, hipStream_t s);
+
 }  // namespace moe

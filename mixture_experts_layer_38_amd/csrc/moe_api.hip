@@ -150,10 +150,13 @@ static moe_status check_debug(const moe_debug_out& D) {
 
 // The launches of one forward pass over the problem's T tokens, with the
 // workspace carved by L (arguments already checked).
+// i8 (NULL for the layer's own weights w1, w3, w2): the experts run on these
+// 8-bit weights, with i8_ws as their workspace.
 static moe_status forward_launch(const moe_problem* p, const ForwardLayout& L, const void* x,
                                  const void* w_router, const void* w1, const void* w3,
                                  const void* w2, const float* logit_bias, void* y,
-                                 const moe_debug_out& D, char* base, hipStream_t s) {
+                                 const moe_debug_out& D, char* base, hipStream_t s,
+                                 const moe_i8_weights* i8 = nullptr, void* i8_ws = nullptr) {
     float* logits = D.logits ? D.logits : (float*)(base + L.logits);
     int32_t* ids = D.topk_ids ? D.topk_ids : (int32_t*)(base + L.ids);
     float* w = D.topk_w ? D.topk_w : (float*)(base + L.w);
@@ -191,11 +194,37 @@ static moe_status forward_launch(const moe_problem* p, const ForwardLayout& L, c
             if (err != hipSuccess) return MOE_ERR_HIP;
         }
     }
-    err = launch_ffn(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, p->dtype, x, row_assign,
-                     offsets, w1, w3, w2, act, h, base + L.ffn_ws, s);
+    if (i8)
+        err = launch_ffn_i8(p->T, p->T * p->top_k, p->top_k, p->n_experts, p->d_model, p->d_ff, x, row_assign,
+                            offsets, *i8, act, h, i8_ws, s);
+    else
+        err = launch_ffn(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, p->dtype, x, row_assign,
+                         offsets, w1, w3, w2, act, h, base + L.ffn_ws, s);
     if (err != hipSuccess) return MOE_ERR_HIP;
     err = launch_combine(p->T, p->top_k, p->d_model, p->dtype, h, assign_row, w, y, s);
     return hip_status(err);
+}
+
+// ---- 8-bit forward --------------------------------------------------------------
+// The products read rows in 16-byte pieces of 8-bit values.
+static moe_status check_i8(const moe_problem* p, const moe_i8_weights* w) {
+    const moe_status st = check_problem(p);
+    if (st != MOE_OK) return st;
+    if (p->dtype != MOE_DTYPE_BF16 || p->d_model % 16 != 0 || p->d_ff % 16 != 0) return MOE_ERR_UNSUPPORTED;
+    if (!w) return MOE_OK;  // a size query
+    REQUIRE(w->w1);
+    REQUIRE(w->w3);
+    REQUIRE(w->w2);
+    REQUIRE(w->s1);
+    REQUIRE(w->s3);
+    REQUIRE(w->s2);
+    return MOE_OK;
+}
+
+// moe_forward's layout (its act, h and routing scratch), then the 8-bit FFN's workspace.
+static size_t forward_i8_ffn_offset(const moe_problem* p) { return align_up(forward_layout(p).total, 256); }
+static size_t forward_i8_ws_bytes(const moe_problem* p) {
+    return forward_i8_ffn_offset(p) + ffn_i8_ws_bytes(p->T, p->T * p->top_k, p->n_experts, p->d_model, p->d_ff);
 }
 
 // ---- allocation-free forward ------------------------------------------------------
@@ -251,7 +280,8 @@ const char* moe_kernel_name(int kid) {
     static const char* names[MOE_KERNEL_COUNT] = {
         "router", "dispatch_count", "dispatch_scan", "dispatch_scatter", "dispatch_gather",
         "ffn_gate_up", "ffn_down", "combine", "aux_loss", "bias_update", "ffn_plan",
-        "router_losses", "ffn"};
+        "router_losses", "ffn", "ffn_train", "ffn_backward", "combine_backward", "route_backward",
+        "quantize", "ffn_i8"};
     return (kid >= 0 && kid < MOE_KERNEL_COUNT) ? names[kid] : "?";
 }
 
@@ -537,6 +567,195 @@ moe_status moe_router_losses(const moe_problem* p, const float* logits, const fl
     return hip_status(launch_router_losses(p->T, p->n_experts, p->top_k, logits, logit_bias,
                                            topk_ids, counts, z_loss, aux_topk, ws,
                                            (hipStream_t)stream));
+}
+
+moe_status moe_expert_ffn_train_workspace_size(const moe_problem* p, size_t* bytes) {
+    moe_status st = check_problem(p);
+    if (st != MOE_OK) return st;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = ffn_train_ws_bytes(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, p->dtype);
+    return MOE_OK;
+}
+
+moe_status moe_expert_ffn_train(const moe_problem* p, const void* x_perm, const int32_t* offsets,
+                                const void* w1, const void* w3, const void* w2, void* gate, void* up,
+                                void* h, void* ws, size_t ws_bytes, void* stream) {
+    moe_status st = check_problem(p);
+    if (st != MOE_OK) return st;
+    REQUIRE(x_perm);
+    REQUIRE(offsets);
+    REQUIRE(w1);
+    REQUIRE(w3);
+    REQUIRE(w2);
+    REQUIRE(gate);
+    REQUIRE(up);
+    REQUIRE(h);
+    if (!ws || ws_bytes < ffn_train_ws_bytes(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, p->dtype))
+        return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
+    return hip_status(launch_ffn_train(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, p->dtype, x_perm,
+                                       offsets, w1, w3, w2, gate, up, h, ws, (hipStream_t)stream));
+}
+
+moe_status moe_expert_ffn_backward_workspace_size(const moe_problem* p, size_t* bytes) {
+    moe_status st = check_problem(p);
+    if (st != MOE_OK) return st;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = ffn_backward_ws_bytes(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, p->dtype);
+    return MOE_OK;
+}
+
+moe_status moe_expert_ffn_backward(const moe_problem* p, const void* x_perm, const int32_t* offsets,
+                                   const void* w1, const void* w3, const void* w2, const void* gate,
+                                   const void* up, const void* dh, void* dx_perm, void* dw1, void* dw3,
+                                   void* dw2, void* ws, size_t ws_bytes, void* stream) {
+    moe_status st = check_problem(p);
+    if (st != MOE_OK) return st;
+    REQUIRE(x_perm);
+    REQUIRE(offsets);
+    REQUIRE(w1);
+    REQUIRE(w3);
+    REQUIRE(w2);
+    REQUIRE(gate);
+    REQUIRE(up);
+    REQUIRE(dh);
+    OPTIONAL(dx_perm);
+    if (dw1 || dw3 || dw2) {  // the three weights' gradients come together
+        REQUIRE(dw1);
+        REQUIRE(dw3);
+        REQUIRE(dw2);
+    } else if (!dx_perm) {
+        return MOE_ERR_INVALID_ARG;
+    }
+    if (!ws || ws_bytes < ffn_backward_ws_bytes(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, p->dtype))
+        return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
+    return hip_status(launch_ffn_backward(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, p->dtype, x_perm,
+                                          offsets, w1, w3, w2, gate, up, dh, dx_perm, dw1, dw3, dw2, ws,
+                                          (hipStream_t)stream));
+}
+
+moe_status moe_combine_backward(const moe_problem* p, const void* dy, const void* h, const int32_t* assign_row,
+                                const float* topk_w, void* dh, float* dtopk_w, void* stream) {
+    moe_status st = check_problem(p);
+    if (st != MOE_OK) return st;
+    REQUIRE(dy);
+    REQUIRE(assign_row);
+    REQUIRE(topk_w);
+    REQUIRE(dh);
+    if (h || dtopk_w) {
+        REQUIRE(h);
+        REQUIRE(dtopk_w);
+    }
+    return hip_status(launch_combine_backward(p->T, p->top_k, p->d_model, p->dtype, dy, h, assign_row, topk_w, dh,
+                                              dtopk_w, (hipStream_t)stream));
+}
+
+moe_status moe_route_backward_workspace_size(const moe_problem* p, size_t* bytes) {
+    moe_status st = check_problem(p);
+    if (st != MOE_OK) return st;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = route_backward_ws_bytes(p->T, p->d_model, p->n_experts);
+    return MOE_OK;
+}
+
+moe_status moe_route_backward(const moe_problem* p, const void* x, const void* w_router, const float* logit_bias,
+                              const float* logits, const int32_t* topk_ids, const float* topk_w,
+                              const float* dtopk_w, const int32_t* counts, float d_aux, float d_z,
+                              const void* dx_perm, const int32_t* assign_row, float* dlogits, void* dx,
+                              void* dw_router, void* ws, size_t ws_bytes, void* stream) {
+    moe_status st = check_problem(p);
+    if (st != MOE_OK) return st;
+    REQUIRE(logits);
+    REQUIRE(topk_ids);
+    REQUIRE(topk_w);
+    REQUIRE(dlogits);
+    OPTIONAL(logit_bias);
+    OPTIONAL(dtopk_w);
+    OPTIONAL(dx_perm);
+    OPTIONAL(assign_row);
+    OPTIONAL(counts);
+    if (d_aux != 0.0f) REQUIRE(counts);
+    if ((dx_perm == nullptr) != (assign_row == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (dx_perm) REQUIRE(dx);  // its sum has nowhere else to go
+    OPTIONAL(dx);
+    if (dx) REQUIRE(w_router);
+    OPTIONAL(dw_router);
+    if (dw_router) {
+        REQUIRE(x);
+        if (!ws || ws_bytes < route_backward_ws_bytes(p->T, p->d_model, p->n_experts)) return MOE_ERR_WORKSPACE;
+        if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
+    }
+    return hip_status(launch_route_backward(p->T, p->d_model, p->n_experts, p->top_k, p->dtype, (int)p->flags, x,
+                                            w_router, logit_bias, logits, topk_ids, topk_w, dtopk_w, counts, d_aux,
+                                            d_z, dx_perm, assign_row, dlogits, dx, dw_router, ws,
+                                            (hipStream_t)stream));
+}
+
+moe_status moe_quantize_rows(int64_t rows, int32_t cols, int32_t dtype, const void* x, int8_t* q, float* scale,
+                             void* stream) {
+    if (rows <= 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (cols % 8 != 0 || cols > 65536 || rows >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+    REQUIRE(x);
+    REQUIRE(q);
+    REQUIRE(scale);
+    return hip_status(launch_quantize_rows(rows, cols, cols, dtype, x, q, scale, nullptr, (hipStream_t)stream));
+}
+
+moe_status moe_expert_ffn_i8_workspace_size(const moe_problem* p, size_t* bytes) {
+    moe_status st = check_i8(p, nullptr);
+    if (st != MOE_OK) return st;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    const int n = p->T * p->top_k;
+    *bytes = ffn_i8_ws_bytes(n, n, p->n_experts, p->d_model, p->d_ff);
+    return MOE_OK;
+}
+
+moe_status moe_expert_ffn_i8(const moe_problem* p, const void* x_perm, const int32_t* offsets,
+                             const moe_i8_weights* w, void* act, void* h, void* ws, size_t ws_bytes,
+                             void* stream) {
+    if (!w) return MOE_ERR_INVALID_ARG;
+    moe_status st = check_i8(p, w);
+    if (st != MOE_OK) return st;
+    REQUIRE(x_perm);
+    REQUIRE(offsets);
+    REQUIRE(act);
+    REQUIRE(h);
+    const int n = p->T * p->top_k;
+    if (!ws || ws_bytes < ffn_i8_ws_bytes(n, n, p->n_experts, p->d_model, p->d_ff)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
+    return hip_status(launch_ffn_i8(n, n, p->top_k, p->n_experts, p->d_model, p->d_ff, x_perm, nullptr, offsets, *w,
+                                    act, h, ws, (hipStream_t)stream));
+}
+
+moe_status moe_forward_i8_workspace_size(const moe_problem* p, size_t* bytes) {
+    moe_status st = check_i8(p, nullptr);
+    if (st != MOE_OK) return st;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = forward_i8_ws_bytes(p);
+    return MOE_OK;
+}
+
+moe_status moe_forward_i8(const moe_problem* p, const void* x, const void* w_router, const moe_i8_weights* w,
+                          const float* logit_bias, void* y, const moe_debug_out* dbg, void* ws,
+                          size_t ws_bytes, void* stream) {
+    if (!w) return MOE_ERR_INVALID_ARG;
+    moe_status st = check_i8(p, w);
+    if (st != MOE_OK) return st;
+    REQUIRE(x);
+    REQUIRE(w_router);
+    REQUIRE(y);
+    OPTIONAL(logit_bias);
+    moe_debug_out none;
+    memset(&none, 0, sizeof none);
+    const moe_debug_out& D = dbg ? *dbg : none;
+    if ((st = check_debug(D)) != MOE_OK) return st;
+    if (!ws || ws_bytes < forward_i8_ws_bytes(p)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
+    char* base = (char*)ws;
+    return forward_launch(p, forward_layout(p), x, w_router, nullptr, nullptr, nullptr, logit_bias, y, D, base,
+                          (hipStream_t)stream, w, base + forward_i8_ffn_offset(p));
 }
 
 moe_status moe_bias_update(const moe_problem* p, const int32_t* counts, float alpha, float* bias,
