@@ -4,15 +4,22 @@
 //   h = (sum_f act_q w2_q) s_act s2
 // The integer sums are exact in 32 bits (at most 65536 * 127 * 127 < 2^31),
 // so their order does not matter; scales and the gate are fp32.
+#include <algorithm>
+
 #include "../device_common.h"
 #include "../launch.h"
 #include "ffn_tiles.h"
 
 namespace moe {
 
+size_t prefill_ws_bytes(int n_rows, int E, int d);
+hipError_t launch_ffn_prefill_i8(int n_rows, int E, int d, int F, const int8_t* xq, const float* xs,
+                                 const int32_t* rowmap, int topk, const int32_t* offsets, const moe_i8_weights& w8,
+                                 bf16* act, int8_t* aq, float* as, int ldf, bf16* h, void* ws, hipStream_t s);
+
 namespace {
 
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
 
 constexpr int I8_ALIGN = 128;  // the quantised rows are padded with zeros to whole 128-byte lines
 constexpr int I8_BM = 128;     // rows per row tile
@@ -94,7 +101,7 @@ I8Layout i8_layout(int n_x, int n, int E, int d, int F) {
     L.aq = L.xs + align_up((size_t)n_x * sizeof(float), 256);
     L.as = L.aq + align_up((size_t)n * L.ldf, 256);
     L.plan = L.as + align_up((size_t)n * sizeof(float), 256);
-    L.total = L.plan + row_plan_bytes(n, E);
+    L.total = L.plan + std::max(row_plan_bytes(n, E), prefill_ws_bytes(n, E, d));
     return L;
 }
 
@@ -108,17 +115,26 @@ hipError_t launch_ffn_i8(int n_x, int n, int K, int E, int d, int F, const void*
     char* base = (char*)ws;
     int8_t *xq = (int8_t*)base + L.xq, *aq = (int8_t*)base + L.aq;
     float *xs = (float*)(base + L.xs), *as = (float*)(base + L.as);
+    // the tiled GEMMs take reductions of one whole 128-byte stage or more
+    const bool tiled = d >= I8_ALIGN && F >= I8_ALIGN;
     timer_before(MOE_KERNEL_FFN_I8, s);
     // grouped rows past the last group are not read; token rows all are
-    hipError_t err = launch_quantize_rows(n_x, d, L.ldx, MOE_DTYPE_BF16, x, xq, xs, rowmap ? nullptr : offsets + E, s);
+    hipError_t err = launch_quantize_rows(n_x, d, L.ldx, tiled, MOE_DTYPE_BF16, x, xq, xs,
+                                          rowmap ? nullptr : offsets + E, s);
     if (err != hipSuccess) return err;
+    if (tiled) {
+        err = launch_ffn_prefill_i8(n, E, d, F, xq, xs, rowmap, K, offsets, w, (bf16*)act, aq, as, L.ldf, (bf16*)h,
+                                    base + L.plan, s);
+        if (err == hipSuccess) timer_after(MOE_KERNEL_FFN_I8, s);
+        return err;
+    }
     RowPlan plan;
     if ((err = launch_row_plan(n, E, I8_BM, offsets, base + L.plan, &plan, s)) != hipSuccess) return err;
     const unsigned mt = (unsigned)row_plan_tiles(n, E, I8_BM);
     ffn_i8_kernel<true><<<dim3(mt, (F + 63) / 64), 256, 0, s>>>(n, F, d, L.ldx, xq, xs, rowmap, K, plan, offsets, w.w1,
                                                                w.s1, w.w3, w.s3, (bf16*)act);
     if ((err = hipGetLastError()) != hipSuccess) return err;
-    if ((err = launch_quantize_rows(n, F, L.ldf, MOE_DTYPE_BF16, act, aq, as, offsets + E, s)) != hipSuccess) return err;
+    if ((err = launch_quantize_rows(n, F, L.ldf, false, MOE_DTYPE_BF16, act, aq, as, offsets + E, s)) != hipSuccess) return err;
     ffn_i8_kernel<false><<<dim3(mt, (d + 63) / 64), 256, 0, s>>>(n, d, F, L.ldf, aq, as, nullptr, 1, plan, offsets,
                                                                 w.w2, w.s2, nullptr, nullptr, (bf16*)h);
     err = hipGetLastError();

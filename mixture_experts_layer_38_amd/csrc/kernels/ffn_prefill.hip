@@ -150,19 +150,52 @@ constexpr int PF_MAX_CPX = 32;  // compute units per XCD the split buffer is siz
 constexpr int PF_DYN_ROUNDS = 2;
 constexpr int PF_DYN_MIN_ROUNDS = 8;
 
+// What a variant of the tiled kernel takes beyond the layer's forward pass:
+// PfKeep (gate/up GEMM of the training pass): both projections are stored too,
+// rounded to bf16; PfScales (8-bit rows and weights): sums of int8 products in
+// int32, scaled by the row's and the weight row's factor in the epilogue.
+struct PfKeep {
+    bf16 *gate, *up;
+};
+struct PfScales {
+    const float *rows, *wa, *wb;
+};
+template <typename... X>
+constexpr bool pf_keeps = (std::is_same<X, PfKeep>::value || ...);
+template <typename... X>
+constexpr bool pf_int8 = (std::is_same<X, PfScales>::value || ...);
+// The extra argument of type T (T() when the variant has none).
+template <typename T>
+__device__ __forceinline__ T pf_extra() {
+    return T{};
+}
+template <typename T, typename X>
+__device__ __forceinline__ T pf_extra(X x) {
+    if constexpr (std::is_same<T, X>::value) return x;
+    else return T{};
+}
+
+// 8-bit rows are addressed in units of two values (the bf16 of the code
+// below), so a stage's 64 units are 128 values of a 128-byte line and
+// everything up to the MFMAs is the same.
 // N: weight rows of one expert (gate/up: F, down: d); K: reduction length,
-// a multiple of PF_BK; n_nt: weight tiles per row tile.  BM: token rows per
+// a multiple of PF_BK (in the 8-bit variant any length from PF_BK on: the
+// last stage takes the weights' last PF_BK units, of which those that the
+// stage before held already meet zeros in the padded rows); n_nt: weight tiles per row tile.  BM: token rows per
 // tile (256, or 128 for small expert groups); NSLOT: LDS stages in the ring.
 // SPLIT = false: every tile except the k-split ones of the last round;
 // SPLIT = true: only the k ranges of those (fp32 partial tiles into part).
-template <bool GATED, int BM, int NSLOT, bool SPLIT>
+template <bool GATED, int BM, int NSLOT, bool SPLIT, typename... X>
 __global__ __launch_bounds__(PF_THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void ffn_prefill_kernel(
     int n_rows, int N, int K, int n_nt, const bf16* __restrict__ A,
     const int32_t* __restrict__ rowmap, int topk, const int32_t* __restrict__ mt_count, const int32_t* __restrict__ mt_expert,
     const int32_t* __restrict__ mt_row0, const int32_t* __restrict__ offsets,
     const bf16* __restrict__ Wa, const bf16* __restrict__ Wb, bf16* __restrict__ out, int cpx,
-    float* __restrict__ part, int32_t* __restrict__ claim, int cus) {
+    float* __restrict__ part, int32_t* __restrict__ claim, int cus, X... extra) {
+    constexpr bool KEEP = pf_keeps<X...>, I8 = pf_int8<X...>;
+    static_assert(!KEEP || (GATED && !I8), "only the gate/up GEMM keeps its projections");
+    typedef typename std::conditional<I8, i32x16, f32x16>::type Acc;
     constexpr int SA = BM * PF_BK;      // bf16 elements of one A stage
     constexpr int SB = PF_BN * PF_BK;   // bf16 elements of one B stage
     constexpr int NTB = BM / 64;        // 32-row token blocks per wave
@@ -246,7 +279,8 @@ void ffn_prefill_kernel(
     const int row0 = tl.row0;
     const int row_end = tl.row_end;
     // k range of this launch unit: all of K, or range kpart of nsplit
-    const int nk_all = K / PF_BK;
+    const int nk_all = I8 ? (K + PF_BK - 1) / PF_BK : K / PF_BK;
+    const int lda = I8 ? nk_all * PF_BK : K;  // row stride of A
     const int ks0 = split ? nk_all * kpart / sp.nsplit : 0;
     const int nk = split ? nk_all * (kpart + 1) / sp.nsplit - ks0 : nk_all;
 
@@ -287,12 +321,17 @@ void ffn_prefill_kernel(
             const int blk = (tr >> 5) & 3;
             const int f = min(nt * 128 + w * 64 + (blk >> 1) * 32 + (tr & 31), N - 1);
             const bf16* W = (blk & 1) ? Wb : Wa;
-            b_src[j] = W + ((size_t)e * N + f) * K + (size_t)ks0 * PF_BK + c * 8;
+            b_src[j] = W + ((size_t)e * N + f) * K + (I8 ? 0 : (size_t)ks0 * PF_BK) + c * 8;
         } else {
             const int nr = min(nt * PF_BN + tr, N - 1);
-            b_src[j] = Wa + ((size_t)e * N + nr) * K + (size_t)ks0 * PF_BK + c * 8;
+            b_src[j] = Wa + ((size_t)e * N + nr) * K + (I8 ? 0 : (size_t)ks0 * PF_BK) + c * 8;
         }
     }
+    // k offset of the weights' stage kt (of the rows': min(kt, nk - 1) * PF_BK)
+    auto b_off = [&](int kt) __attribute__((always_inline)) {
+        if constexpr (I8) return (size_t)min((ks0 + min(kt, nk - 1)) * PF_BK, K - PF_BK);
+        else return (size_t)min(kt, nk - 1) * PF_BK;
+    };
     // nja: the A loads of a stage (NJA, or the tile's token blocks in the 1 x 4 layout)
     auto issue_a = [&](int kt, bf16* dA, auto nja) __attribute__((always_inline)) {
         const size_t ko = (size_t)min(kt, nk - 1) * PF_BK;
@@ -303,7 +342,7 @@ void ffn_prefill_kernel(
                                              16, 0, 0);
     };
     auto issue_b = [&](int kt, bf16* dB) __attribute__((always_inline)) {
-        const size_t ko = (size_t)min(kt, nk - 1) * PF_BK;
+        const size_t ko = b_off(kt);
 #pragma unroll
         for (int j = 0; j < NJB; ++j)
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(b_src[j] + ko),
@@ -352,17 +391,17 @@ void ffn_prefill_kernel(
         // assignment -> token (src_row): a dropped slot (-1) reads token 0
         const int a = pf_opaque_v(arow[j]);  // waited for here, after the weights' loads
         const int r = rowmap != nullptr ? (a < 0 ? 0 : a / topk) : a;
-        a_src[j] = A + (size_t)r * K + (size_t)ks0 * PF_BK + (ls ^ pf_swz(tr)) * 8;
+        a_src[j] = A + (size_t)r * lda + (size_t)ks0 * PF_BK + (ls ^ pf_swz(tr)) * 8;
     }
     // acc[wb + 2 (tb / 4)][tb % 4]: the accumulators of weight block wb and
     // token block tb (4 x NTB blocks in the 2 x 2 layout, 2 x 2 NTB in 1 x 4).
-    f32x16 acc[4][NTB];
+    Acc acc[4][NTB];
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int b = 0; b < NTB; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0;
 
     // Fragment rows: weight rows wrow0 + 32 wb + lane%32, token rows
     // trow0 + 32 tb + lane%32; their swizzles are fixed for the whole tile.
@@ -397,8 +436,9 @@ void ffn_prefill_kernel(
         for (int wb = 0; wb < WB; ++wb)
 #pragma unroll
             for (int tb = 0; tb < NB; ++tb) {
-                f32x16& a = acc[wb + 2 * (tb >> 2)][tb & 3];
-                a = mfma32(f.w[wb], f.t[tb], a);
+                Acc& a = acc[wb + 2 * (tb >> 2)][tb & 3];
+                if constexpr (I8) a = mfma32_i8(f.w[wb], f.t[tb], a);
+                else a = mfma32(f.w[wb], f.t[tb], a);
             }
     };
     // Interleave: one MFMA, then one LDS fragment read, for every read of the
@@ -492,7 +532,7 @@ void ffn_prefill_kernel(
         constexpr int NL = SW ? NJ : NJB;  // loads after the barrier
         constexpr int V0 = (NE + 2) / 3, V1 = (NE + 1) / 3, V2 = NE / 3;
         static_assert(V0 + V1 + V2 == NE, "early loads per quarter");
-        const size_t ko = (size_t)min(kt + 2, nk - 1) * PF_BK;
+        const size_t ko = SW ? b_off(kt + 2) : (size_t)min(kt + 2, nk - 1) * PF_BK;
         auto ld = [&](int j) __attribute__((always_inline)) {
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((SW ? b_src[j] : a_src[j]) + ko),
                                              (__attribute__((address_space(3))) void*)(pA + 8 * (wave + 4 * j) * PF_BK),
@@ -543,13 +583,14 @@ void ffn_prefill_kernel(
         constexpr int V0 = V, V1 = V, V2 = V, V3 = NLD - 3 * V;
         static_assert(V3 >= 0, "loads per quarter");
         const size_t ko = (size_t)min(kt + 2, nk - 1) * PF_BK;
+        const size_t kob = b_off(kt + 2);
         auto ld = [&](int i) __attribute__((always_inline)) {
             if (i < NJA)
                 __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(a_src[i] + ko),
                                                  (__attribute__((address_space(3))) void*)(pA + 8 * (wave + 4 * i) * PF_BK),
                                                  16, 0, 0);
             else
-                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(b_src[i - NJA] + ko),
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(b_src[i - NJA] + kob),
                                                  (__attribute__((address_space(3))) void*)(pB + 8 * (wave + 4 * (i - NJA)) * PF_BK),
                                                  16, 0, 0);
         };
@@ -767,10 +808,11 @@ void ffn_prefill_kernel(
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int wb = 0; wb < WBN; ++wb) {
-                        const f32x16& a = acc[wb + 2 * (tb >> 2)][tb & 3];
+                        const Acc& a = acc[wb + 2 * (tb >> 2)][tb & 3];
                         const int cl = wb * 32 + 8 * q + 4 * (el >> 5);
+                        // (8-bit variant: the bits of the int32 sums)
                         *reinterpret_cast<f32x4*>(sf + rl * W + (((cl >> 2) ^ (rl & 7)) << 2)) =
-                            f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+                            f32x4{pf_bits(a[4 * q]), pf_bits(a[4 * q + 1]), pf_bits(a[4 * q + 2]), pf_bits(a[4 * q + 3])};
                     }
             }
             const int lrow = el / NCH, lch = el % NCH;
@@ -782,8 +824,19 @@ void ffn_prefill_kernel(
             }
         }
     };
-    auto store_tile = [&](auto wbn_c, auto tbn_c) __attribute__((always_inline)) {
+    // 8-bit variant: the factor of local token row rl, and those of four weight
+    // rows from tile weight row wr on (gate/up: their features')
+    const PfScales sc = pf_extra<PfScales>(extra...);
+    auto row_scale = [&](int rl) __attribute__((always_inline)) {
+        return sc.rows[src_row(rowmap, topk, min(row0 + trow0 + rl, row_end - 1))];
+    };
+    auto col_scale = [&](const float* p, int col) __attribute__((always_inline)) {
+        return *reinterpret_cast<const f32x4*>(p + (size_t)e * N + min(col, N - 4));
+    };
+    // WHICH: the output itself (gate/up: act), or the gate (1) or up (2) projection
+    auto store_tile = [&](auto wbn_c, auto tbn_c, auto which_c, bf16* dst) __attribute__((always_inline)) {
         constexpr int WBN = decltype(wbn_c)::value, TBN = decltype(tbn_c)::value;
+        constexpr int WHICH = decltype(which_c)::value;
         constexpr int W = (GATED ? 16 : 32) * WBN;  // bf16 columns of the wave's block
         constexpr int NCH = W / 8;                   // 16-byte chunks per row
         constexpr int SWM = NCH < 8 ? NCH - 1 : 7;   // chunk swizzle: chunk ^ (row & SWM)
@@ -791,11 +844,16 @@ void ffn_prefill_kernel(
         // a wave's block fits its unit (the ring's 32 KB units; else the
         // smallest slot used, an A slot)
         static_assert(TBN * 32 * W * (int)sizeof(bf16) <= UNIT, "a wave's block fits its LDS unit");
+        // columns of the wave's block in the output: features nt*128 +
+        // wrow0 / 2 (gate/up), or weight rows nt*256 + wrow0 (N a multiple of 8)
+        const int colbase = GATED ? nt * 128 + wrow0 / 2 : nt * PF_BN + wrow0;
 #pragma unroll
         for (int tb = 0; tb < TBN; ++tb) {
             if (tb >= tbn) continue;
             const int rl = tb * 32 + (el & 31);
             bf16* srow = st + rl * W;
+            float rs = 0.0f;
+            if constexpr (I8) rs = row_scale(rl);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int wr = 8 * q + 4 * (el >> 5);
@@ -804,29 +862,44 @@ void ffn_prefill_kernel(
                     for (int pr = 0; pr < WBN / 2; ++pr) {
                         // the wave's weight rows interleave W1 and W3 in
                         // 32-row blocks: local features pr*32 + wr + [0, 4)
-                        float v[4];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            v[r] = silu(acc[2 * pr + 2 * (tb >> 2)][tb & 3][4 * q + r]) *
-                                   acc[2 * pr + 1 + 2 * (tb >> 2)][tb & 3][4 * q + r];
+                        const Acc& ga = acc[2 * pr + 2 * (tb >> 2)][tb & 3];
+                        const Acc& ua = acc[2 * pr + 1 + 2 * (tb >> 2)][tb & 3];
                         const int cl = pr * 32 + wr;
+                        float v[4];
+                        if constexpr (I8) {
+                            const f32x4 s1 = col_scale(sc.wa, colbase + cl), s3 = col_scale(sc.wb, colbase + cl);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                v[r] = silu((float)ga[4 * q + r] * rs * s1[r]) * ((float)ua[4 * q + r] * rs * s3[r]);
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                v[r] = WHICH == 0 ? silu(ga[4 * q + r]) * ua[4 * q + r]
+                                                  : WHICH == 1 ? ga[4 * q + r] : ua[4 * q + r];
+                        }
                         *reinterpret_cast<bf16x4*>(srow + (((cl >> 3) ^ (rl & SWM)) << 3) + (cl & 7)) =
                             bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
                     }
                 } else {
 #pragma unroll
                     for (int wb = 0; wb < WBN; ++wb) {
-                        const f32x16& av = acc[wb + 2 * (tb >> 2)][tb & 3];
+                        const Acc& av = acc[wb + 2 * (tb >> 2)][tb & 3];
                         const int cl = wb * 32 + wr;
+                        float v[4];
+                        if constexpr (I8) {
+                            const f32x4 s1 = col_scale(sc.wa, colbase + cl);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) v[r] = (float)av[4 * q + r] * rs * s1[r];
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) v[r] = av[4 * q + r];
+                        }
                         *reinterpret_cast<bf16x4*>(srow + (((cl >> 3) ^ (rl & SWM)) << 3) + (cl & 7)) =
-                            bf16x4{(bf16)av[4 * q], (bf16)av[4 * q + 1], (bf16)av[4 * q + 2], (bf16)av[4 * q + 3]};
+                            bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
                     }
                 }
             }
         }
-        // columns of the wave's block in the output: features nt*128 +
-        // wrow0 / 2 (gate/up), or weight rows nt*256 + wrow0 (N a multiple of 8)
-        const int colbase = GATED ? nt * 128 + wrow0 / 2 : nt * PF_BN + wrow0;
         const int lrow = el / NCH, lch = el % NCH;
         const int gcol = colbase + lch * 8;
 #pragma unroll
@@ -834,14 +907,20 @@ void ffn_prefill_kernel(
             const int rl = i * RPI + lrow;
             const int grow = row0 + trow0 + rl;
             const bf16x8 val = *reinterpret_cast<const bf16x8*>(st + rl * W + ((lch ^ (rl & SWM)) << 3));
-            if (grow < row_end && gcol < N) *reinterpret_cast<bf16x8*>(out + (size_t)grow * N + gcol) = val;
+            if (grow < row_end && gcol < N) *reinterpret_cast<bf16x8*>(dst + (size_t)grow * N + gcol) = val;
         }
     };
     auto store = [&](auto wbn_c, auto tbn_c) __attribute__((always_inline)) {
         if constexpr (SPLIT)
             store_part(wbn_c, tbn_c);
         else
-            store_tile(wbn_c, tbn_c);
+            store_tile(wbn_c, tbn_c, std::integral_constant<int, 0>{}, out);
+        if constexpr (KEEP) {
+            // each wave's unit takes the projections in turn (its LDS accesses stay in order)
+            const PfKeep keep = pf_extra<PfKeep>(extra...);
+            store_tile(wbn_c, tbn_c, std::integral_constant<int, 1>{}, keep.gate);
+            store_tile(wbn_c, tbn_c, std::integral_constant<int, 2>{}, keep.up);
+        }
     };
     if constexpr (HALF) {
         if (ht)
@@ -866,13 +945,13 @@ constexpr size_t PG_LDS_BYTES = 4 * PG_TILE_ELEMS * sizeof(bf16);
 // Generic variant for any K (a multiple of 8): the same tiles, with operands
 // staged HBM/L2 -> registers -> LDS (rows padded to 144 bytes), double
 // buffered with one 64-wide k step in flight.  N, K, n_nt as above.
-template <bool GATED>
+template <bool GATED, typename... X>
 __global__ __launch_bounds__(PG_THREADS) void ffn_prefill_generic_kernel(
     int n_rows, int N, int K, int n_nt, const bf16* __restrict__ A,
     const int32_t* __restrict__ rowmap, int topk, const int32_t* __restrict__ mt_count,
     const int32_t* __restrict__ mt_expert, const int32_t* __restrict__ mt_row0,
     const int32_t* __restrict__ offsets, const bf16* __restrict__ Wa, const bf16* __restrict__ Wb,
-    bf16* __restrict__ out) {
+    bf16* __restrict__ out, X... extra) {
     extern __shared__ __align__(16) bf16 smem[];
     const int n_mt = *mt_count;
     const int tiles = n_mt * n_nt;
@@ -993,6 +1072,16 @@ __global__ __launch_bounds__(PG_THREADS) void ffn_prefill_generic_kernel(
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         v[r] = silu(acc[2 * pr][tb][4 * q + r]) * acc[2 * pr + 1][tb][4 * q + r];
+                    if constexpr (pf_keeps<X...>) {  // N is a multiple of 8
+                        const PfKeep keep = pf_extra<PfKeep>(extra...);
+                        const f32x16 &ga = acc[2 * pr][tb], &ua = acc[2 * pr + 1][tb];
+                        if (f < N) {
+                            *reinterpret_cast<bf16x4*>(keep.gate + (size_t)grow * N + f) =
+                                bf16x4{(bf16)ga[4 * q], (bf16)ga[4 * q + 1], (bf16)ga[4 * q + 2], (bf16)ga[4 * q + 3]};
+                            *reinterpret_cast<bf16x4*>(keep.up + (size_t)grow * N + f) =
+                                bf16x4{(bf16)ua[4 * q], (bf16)ua[4 * q + 1], (bf16)ua[4 * q + 2], (bf16)ua[4 * q + 3]};
+                        }
+                    }
                     if (f + 3 < N) {
                         bf16x4 pk = {(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
                         *reinterpret_cast<bf16x4*>(orow + f) = pk;
@@ -1026,11 +1115,13 @@ __global__ __launch_bounds__(PG_THREADS) void ffn_prefill_generic_kernel(
 // once (PF_RD_V float4 of each partial tile).
 constexpr int PF_RD_ROWS = 16;
 constexpr int PF_RD_V = PF_RD_ROWS * PF_BN / 4 / 256;
-template <int BM>
+template <int BM, typename... X>
 __global__ __launch_bounds__(256) void ffn_split_reduce_kernel(
     int n_rows, int N, int n_nt, int cpx, const int32_t* __restrict__ mt_count,
     const int32_t* __restrict__ mt_expert, const int32_t* __restrict__ mt_row0,
-    const int32_t* __restrict__ offsets, const float* __restrict__ part, bf16* __restrict__ out) {
+    const int32_t* __restrict__ offsets, const float* __restrict__ part, bf16* __restrict__ out, X... extra) {
+    constexpr bool I8 = pf_int8<X...>;
+    typedef typename std::conditional<I8, i32x4, f32x4>::type Vec;
     const int n_mt = *mt_count;
     const int tiles = n_mt * n_nt;
     const int per_xcd = (tiles + PF_XCD - 1) / PF_XCD;
@@ -1045,13 +1136,13 @@ __global__ __launch_bounds__(256) void ffn_split_reduce_kernel(
     if (tl.row0 + rb >= tl.row_end) return;
     const size_t tsz = (size_t)BM * PF_BN;
     const float* p0 = part + (size_t)((xcd * sp.rem + r) * sp.nsplit) * tsz + (size_t)rb * PF_BN;
-    f32x4 v[PF_RD_V];
+    Vec v[PF_RD_V];
 #pragma unroll
-    for (int u = 0; u < PF_RD_V; ++u) v[u] = *reinterpret_cast<const f32x4*>(p0 + (u * 256 + threadIdx.x) * 4);
+    for (int u = 0; u < PF_RD_V; ++u) v[u] = *reinterpret_cast<const Vec*>(p0 + (u * 256 + threadIdx.x) * 4);
     for (int p = 1; p < sp.nsplit; ++p)
 #pragma unroll
         for (int u = 0; u < PF_RD_V; ++u)
-            v[u] += *reinterpret_cast<const f32x4*>(p0 + p * tsz + (u * 256 + threadIdx.x) * 4);
+            v[u] += *reinterpret_cast<const Vec*>(p0 + p * tsz + (u * 256 + threadIdx.x) * 4);
 #pragma unroll
     for (int u = 0; u < PF_RD_V; ++u) {
         const int i = (u * 256 + threadIdx.x) * 4;
@@ -1059,6 +1150,14 @@ __global__ __launch_bounds__(256) void ffn_split_reduce_kernel(
         const int gcol = tl.nt * PF_BN + i % PF_BN;
         if (grow >= tl.row_end || gcol >= N) continue;
         bf16* o = out + (size_t)grow * N + gcol;
+        if constexpr (I8) {  // N is a multiple of 16
+            const PfScales sc = pf_extra<PfScales>(extra...);
+            const f32x4 s1 = *reinterpret_cast<const f32x4*>(sc.wa + (size_t)tl.e * N + gcol);
+            const float rs = sc.rows[grow];
+            *reinterpret_cast<bf16x4*>(o) = bf16x4{(bf16)((float)v[u][0] * rs * s1[0]), (bf16)((float)v[u][1] * rs * s1[1]),
+                                                   (bf16)((float)v[u][2] * rs * s1[2]), (bf16)((float)v[u][3] * rs * s1[3])};
+            continue;
+        }
         if (gcol + 3 < N) {
             *reinterpret_cast<bf16x4*>(o) = bf16x4{(bf16)v[u][0], (bf16)v[u][1], (bf16)v[u][2], (bf16)v[u][3]};
         } else {
@@ -1113,7 +1212,7 @@ hipError_t launch_row_plan(int n_rows, int E, int bm, const int32_t* offsets, vo
 // concurrent first calls from several threads are safe); a failure is kept
 // and returned by every later call on that device.
 constexpr int PG_MAX_DEVICES = 64;
-template <bool GATED>
+template <bool GATED, typename... X>
 static hipError_t generic_lds_attr() {
     static std::once_flag once[PG_MAX_DEVICES];
     static hipError_t result[PG_MAX_DEVICES];
@@ -1122,7 +1221,7 @@ static hipError_t generic_lds_attr() {
     if (err != hipSuccess) return err;
     if (dev < 0 || dev >= PG_MAX_DEVICES) return hipErrorInvalidDevice;
     std::call_once(once[dev], [dev] {
-        result[dev] = hipFuncSetAttribute((const void*)ffn_prefill_generic_kernel<GATED>,
+        result[dev] = hipFuncSetAttribute((const void*)ffn_prefill_generic_kernel<GATED, X...>,
                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)PG_LDS_BYTES);
     });
     return result[dev];
@@ -1132,13 +1231,14 @@ static hipError_t generic_lds_attr() {
 // multiple of 8 (its output leaves in 16-byte row chunks).
 static bool pf_tiled_ok(int N, int K) { return K % PF_BK == 0 && N % 8 == 0; }
 
-template <bool GATED>
+// K: in PF_BK units of the element (8-bit variant: of two values)
+template <bool GATED, typename... X>
 static hipError_t launch_prefill_gemm(int n_rows, int N, int K, int n_nt, int max_mt, int bm, int E,
                                       const bf16* A, const int32_t* rowmap, int topk,
                                       const int32_t* mt_count,
                                       const int32_t* mt_expert, const int32_t* mt_row0,
                                       const int32_t* offsets, const bf16* Wa, const bf16* Wb,
-                                      bf16* out, float* part, int32_t* claim, hipStream_t s) {
+                                      bf16* out, float* part, int32_t* claim, hipStream_t s, X... extra) {
     // Workgroups for the plan's row tiles: the groups hold at most n_rows rows
     // (offsets is a prefix sum ending at or below n_rows), so there are at
     // most n_rows / bm full tiles plus one partly filled tile per expert.
@@ -1147,7 +1247,7 @@ static hipError_t launch_prefill_gemm(int n_rows, int N, int K, int n_nt, int ma
     // at the end of the launch, only to exit.
     const long mts = std::min((long)max_mt, (long)n_rows / bm + E + 1);
     const long tiles = mts * n_nt;
-    if (pf_tiled_ok(N, K)) {
+    if (pf_int8<X...> || pf_tiled_ok(N, K)) {
         const int cus = prefill_cpx();  // compute units per XCD (0: unknown)
         // the second GEMM may cut its last round into k ranges (K >= 4 stages)
         const int cpx = (!GATED && K / PF_BK >= 4) ? cus : 0;
@@ -1157,39 +1257,45 @@ static hipError_t launch_prefill_gemm(int n_rows, int N, int K, int n_nt, int ma
         const unsigned grid = (unsigned)(((tiles + PF_XCD - 1) / PF_XCD + xc) * PF_XCD);
         const unsigned sgrid = (unsigned)(PF_XCD * cpx);  // split units: at most cpx per XCD
         if (bm == 256)
-            ffn_prefill_kernel<GATED, 256, 5, false><<<grid, PF_THREADS, 0, s>>>(
+            ffn_prefill_kernel<GATED, 256, 5, false, X...><<<grid, PF_THREADS, 0, s>>>(
                 n_rows, N, K, n_nt, A, rowmap, topk, mt_count, mt_expert, mt_row0, offsets, Wa, Wb, out, cpx, part,
-                claim, xc);
+                claim, xc, extra...);
         else
-            ffn_prefill_kernel<GATED, 128, 3, false><<<grid, PF_THREADS, 0, s>>>(
+            ffn_prefill_kernel<GATED, 128, 3, false, X...><<<grid, PF_THREADS, 0, s>>>(
                 n_rows, N, K, n_nt, A, rowmap, topk, mt_count, mt_expert, mt_row0, offsets, Wa, Wb, out, cpx, part,
-                claim, xc);
+                claim, xc, extra...);
         hipError_t err = hipGetLastError();
-        if (err != hipSuccess || cpx == 0 || GATED) return err;
+        if constexpr (GATED) return err;
+        else {
+        if (err != hipSuccess || cpx == 0) return err;
         if (bm == 256)
-            ffn_prefill_kernel<false, 256, 5, true><<<sgrid, PF_THREADS, 0, s>>>(
+            ffn_prefill_kernel<false, 256, 5, true, X...><<<sgrid, PF_THREADS, 0, s>>>(
                 n_rows, N, K, n_nt, A, rowmap, topk, mt_count, mt_expert, mt_row0, offsets, Wa, Wb, out, cpx, part,
-                nullptr, 0);
+                nullptr, 0, extra...);
         else
-            ffn_prefill_kernel<false, 128, 3, true><<<sgrid, PF_THREADS, 0, s>>>(
+            ffn_prefill_kernel<false, 128, 3, true, X...><<<sgrid, PF_THREADS, 0, s>>>(
                 n_rows, N, K, n_nt, A, rowmap, topk, mt_count, mt_expert, mt_row0, offsets, Wa, Wb, out, cpx, part,
-                nullptr, 0);
+                nullptr, 0, extra...);
         if ((err = hipGetLastError()) != hipSuccess) return err;
         const dim3 rgrid((unsigned)(PF_XCD * (cpx / 2)), (unsigned)(bm / PF_RD_ROWS));
         if (bm == 256)
-            ffn_split_reduce_kernel<256><<<rgrid, 256, 0, s>>>(n_rows, N, n_nt, cpx, mt_count, mt_expert, mt_row0,
-                                                               offsets, part, out);
+            ffn_split_reduce_kernel<256, X...><<<rgrid, 256, 0, s>>>(n_rows, N, n_nt, cpx, mt_count, mt_expert, mt_row0,
+                                                               offsets, part, out, extra...);
         else
-            ffn_split_reduce_kernel<128><<<rgrid, 256, 0, s>>>(n_rows, N, n_nt, cpx, mt_count, mt_expert, mt_row0,
-                                                               offsets, part, out);
+            ffn_split_reduce_kernel<128, X...><<<rgrid, 256, 0, s>>>(n_rows, N, n_nt, cpx, mt_count, mt_expert, mt_row0,
+                                                               offsets, part, out, extra...);
         return hipGetLastError();
+        }
     }
+    if constexpr (pf_int8<X...>) return hipErrorInvalidValue;
+    else {
     const unsigned grid = (unsigned)((((long)max_mt * n_nt + PF_XCD - 1) / PF_XCD) * PF_XCD);
-    hipError_t aerr = generic_lds_attr<GATED>();
+    hipError_t aerr = generic_lds_attr<GATED, X...>();
     if (aerr != hipSuccess) return aerr;
-    ffn_prefill_generic_kernel<GATED><<<grid, PG_THREADS, PG_LDS_BYTES, s>>>(
-        n_rows, N, K, n_nt, A, rowmap, topk, mt_count, mt_expert, mt_row0, offsets, Wa, Wb, out);
+    ffn_prefill_generic_kernel<GATED, X...><<<grid, PG_THREADS, PG_LDS_BYTES, s>>>(
+        n_rows, N, K, n_nt, A, rowmap, topk, mt_count, mt_expert, mt_row0, offsets, Wa, Wb, out, extra...);
     return hipGetLastError();
+    }
 }
 
 // Row-tile height: 256 when the expert groups hold at least 128 rows on
@@ -1248,6 +1354,66 @@ hipError_t launch_ffn_prefill(int n_rows, int E, int d, int F, const void* A, co
     }
     timer_after(MOE_KERNEL_FFN_DOWN, s);
     return hipSuccess;
+}
+
+// Workspace of the two variants below: prefill_ws_bytes.
+struct PfWs {
+    int max_mt;
+    int32_t *mt_count, *mt_expert, *mt_row0, *small_count, *small_list, *claim;
+    float* part;
+};
+static PfWs pf_ws(int n_rows, int E, void* ws) {
+    PfWs w;
+    w.max_mt = prefill_max_mtiles(n_rows, E);
+    w.mt_count = reinterpret_cast<int32_t*>(ws);
+    w.mt_expert = w.mt_count + 1;
+    w.mt_row0 = w.mt_expert + w.max_mt;
+    w.small_count = w.mt_row0 + w.max_mt;
+    w.small_list = w.small_count + 1;
+    w.claim = w.small_list + E;
+    w.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + prefill_plan_bytes(n_rows, E));
+    return w;
+}
+
+// The training pass: every expert on the tiled GEMMs, gate and up kept.
+hipError_t launch_ffn_prefill_keep(int n_rows, int E, int d, int F, const bf16* x, const int32_t* offsets,
+                                   const bf16* w1, const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act,
+                                   bf16* h, void* ws, hipStream_t s) {
+    const PfWs w = pf_ws(n_rows, E, ws);
+    const int bm = prefill_bm(n_rows, E, d, F);
+    ffn_plan_kernel<<<1, 1024, 0, s>>>(E, w.max_mt, bm, 0, offsets, w.mt_count, w.mt_expert, w.mt_row0, w.small_count,
+                                       w.small_list, w.claim);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    err = launch_prefill_gemm<true>(n_rows, F, d, (F + 127) / 128, w.max_mt, bm, E, x, nullptr, 1, w.mt_count,
+                                    w.mt_expert, w.mt_row0, offsets, w1, w3, act, nullptr, w.claim, s, PfKeep{gate, up});
+    if (err != hipSuccess) return err;
+    return launch_prefill_gemm<false>(n_rows, d, F, (d + PF_BN - 1) / PF_BN, w.max_mt, bm, E, act, nullptr, 1,
+                                      w.mt_count, w.mt_expert, w.mt_row0, offsets, w2, nullptr, h, w.part,
+                                      w.claim + PF_XCD, s);
+}
+
+// 8-bit experts (d and F at least 128).  xq: the quantised grouped rows, or
+// with a row map the tokens'; quantize_act runs between the two GEMMs.
+hipError_t launch_ffn_prefill_i8(int n_rows, int E, int d, int F, const int8_t* xq, const float* xs,
+                                 const int32_t* rowmap, int topk, const int32_t* offsets, const moe_i8_weights& w8,
+                                 bf16* act, int8_t* aq, float* as, int ldf, bf16* h, void* ws, hipStream_t s) {
+    const PfWs w = pf_ws(n_rows, E, ws);
+    const int bm = n_rows >= 128 * E ? 256 : 128;  // as prefill_bm
+    ffn_plan_kernel<<<1, 1024, 0, s>>>(E, w.max_mt, bm, 0, offsets, w.mt_count, w.mt_expert, w.mt_row0, w.small_count,
+                                       w.small_list, w.claim);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const auto unit = [](const int8_t* v) { return reinterpret_cast<const bf16*>(v); };  // two values
+    err = launch_prefill_gemm<true>(n_rows, F, d / 2, (F + 127) / 128, w.max_mt, bm, E, unit(xq), rowmap, topk,
+                                    w.mt_count, w.mt_expert, w.mt_row0, offsets, unit(w8.w1), unit(w8.w3), act, nullptr,
+                                    w.claim, s, PfScales{xs, w8.s1, w8.s3});
+    if (err != hipSuccess) return err;
+    if ((err = launch_quantize_rows(n_rows, F, ldf, true, MOE_DTYPE_BF16, act, aq, as, offsets + E, s)) != hipSuccess)
+        return err;
+    return launch_prefill_gemm<false>(n_rows, d, F / 2, (d + PF_BN - 1) / PF_BN, w.max_mt, bm, E, unit(aq), nullptr, 1,
+                                      w.mt_count, w.mt_expert, w.mt_row0, offsets, unit(w8.w2), nullptr, h, w.part,
+                                      w.claim + PF_XCD, s, PfScales{as, w8.s2, nullptr});
 }
 
 // A plain linear layer (one group of n_rows rows) on the second GEMM's

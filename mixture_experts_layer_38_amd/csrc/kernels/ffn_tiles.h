@@ -20,6 +20,10 @@ __device__ __forceinline__ int pf_swz(int r) { return (r ^ (r >> 3)) & 7; }
 // s_waitcnt immediate: lgkmcnt == 0, no wait on the other counters.
 #define PF_WAIT_LGKM0() __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14))
 
+// The 32 bits of an accumulator element as a float (for stores that move both kinds).
+__device__ __forceinline__ float pf_bits(float v) { return v; }
+__device__ __forceinline__ float pf_bits(int v) { return __builtin_bit_cast(float, v); }
+
 // v itself, passed through an empty asm statement (no instruction): the
 // compiler keeps it after the memory operations issued before it, so a load
 // whose value goes through it is waited for only here.

@@ -13,6 +13,11 @@
 
 namespace moe {
 
+size_t prefill_ws_bytes(int n_rows, int E, int d);
+hipError_t launch_ffn_prefill_keep(int n_rows, int E, int d, int F, const bf16* x, const int32_t* offsets,
+                                   const bf16* w1, const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act,
+                                   bf16* h, void* ws, hipStream_t s);
+
 namespace {
 
 // ---- fp32 path -------------------------------------------------------------------
@@ -65,9 +70,10 @@ struct EpiWeights {  // C is one expert's [M][N]
     }
 };
 
-template <typename T>
-hipError_t train_gemms(int n, int E, int d, int F, const T* x, const int32_t* offsets, const T* w1, const T* w3,
-                       const T* w2, T* gate, T* up, T* act, T* h, const RowPlan& plan, hipStream_t s) {
+hipError_t train_gemms(int n, int E, int d, int F, const float* x, const int32_t* offsets, const float* w1,
+                       const float* w3, const float* w2, float* gate, float* up, float* act, float* h,
+                       const RowPlan& plan, hipStream_t s) {
+    typedef float T;
     const unsigned mt = (unsigned)row_plan_tiles(n, E, GM_T);
     GemmArgs<T, T> g{{x, nullptr}, {w1, w3}, d, d, (size_t)F * d, 0, F, d, n, E, plan, offsets};
     gemm_f32_kernel<GM_NT, true, 1, true, true><<<dim3(mt, (F + GM_T - 1) / GM_T), 256, 0, s>>>(
@@ -110,10 +116,11 @@ hipError_t backward_gemms(int n, int E, int d, int F, const T* x, const int32_t*
 
 }  // namespace
 
-// act, then the row plan
+// act, then the row plan (bf16: the tiled GEMMs' workspace)
 size_t ffn_train_ws_bytes(int T, int K, int E, int d, int F, int dtype) {
     const size_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
-    return align_up((size_t)T * K * F * es, 256) + row_plan_bytes(T * K, E);
+    return align_up((size_t)T * K * F * es, 256) +
+           (dtype == MOE_DTYPE_F32 ? row_plan_bytes(T * K, E) : prefill_ws_bytes(T * K, E, d));
 }
 
 hipError_t launch_ffn_train(int T, int K, int E, int d, int F, int dtype, const void* x, const int32_t* offsets,
@@ -122,16 +129,18 @@ hipError_t launch_ffn_train(int T, int K, int E, int d, int F, int dtype, const 
     const int n = T * K;
     const size_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
     char* base = (char*)ws;
-    RowPlan plan;
+    void* rest = base + align_up((size_t)n * F * es, 256);
+    hipError_t err;
     timer_before(MOE_KERNEL_FFN_TRAIN, s);
-    hipError_t err = launch_row_plan(n, E, GM_T, offsets, base + align_up((size_t)n * F * es, 256), &plan, s);
-    if (err != hipSuccess) return err;
-    if (dtype == MOE_DTYPE_F32)
-        err = train_gemms<float>(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3,
-                                  (const float*)w2, (float*)gate, (float*)up, (float*)base, (float*)h, plan, s);
-    else
-        err = train_gemms<bf16>(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3,
-                                (const bf16*)w2, (bf16*)gate, (bf16*)up, (bf16*)base, (bf16*)h, plan, s);
+    if (dtype == MOE_DTYPE_F32) {
+        RowPlan plan;
+        if ((err = launch_row_plan(n, E, GM_T, offsets, rest, &plan, s)) != hipSuccess) return err;
+        err = train_gemms(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3, (const float*)w2,
+                          (float*)gate, (float*)up, (float*)base, (float*)h, plan, s);
+    } else {
+        err = launch_ffn_prefill_keep(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3,
+                                      (const bf16*)w2, (bf16*)gate, (bf16*)up, (bf16*)base, (bf16*)h, rest, s);
+    }
     if (err == hipSuccess) timer_after(MOE_KERNEL_FFN_TRAIN, s);
     return err;
 }

@@ -29,9 +29,11 @@ __device__ __forceinline__ int quantize_one(float x, float scale, float inv) {
 // the row reads cached lines.  A row holding a NaN or an infinity gets a NaN
 // scale (its bits pass every finite value's) and zeros, so what is computed
 // from it is NaN.  live: rows at or past *live are left alone (NULL: none);
-// columns [cols, ldq) of q are written as zeros.
+// bytes [cols, ldq) of q are written as zeros; byte p of q at or past split
+// (a multiple of 128, cols - split < 128) holds column p - split + cols - 128,
+// zero where that lies before split.
 template <typename T, int TPR>
-__global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t rows, int cols, int ldq, const T* __restrict__ x,
+__global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t rows, int cols, int ldq, int split, const T* __restrict__ x,
                                                            int8_t* __restrict__ q, float* __restrict__ scale,
                                                            const int32_t* __restrict__ live) {
     constexpr int RPB = 256 / TPR;  // rows per block
@@ -77,9 +79,10 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t rows, int co
         const float s = fmaxf(__builtin_bit_cast(float, m) / 127.0f, 0x1p-126f);
         const float inv = finite ? 1.0f / s : 0.0f;
         if (i == 0) scale[r] = finite ? s : __builtin_nanf("");
-        for (int c = i * 8; c < ldq; c += TPR * 8) {
+        for (int b = i * 8; b < ldq; b += TPR * 8) {
+            const int c = b < split ? b : b - split + cols - 128;
             uint32_t lo = 0, hi = 0;
-            if (c < cols && finite) {
+            if ((b < split || c >= split) && c < cols && finite) {
                 float v[8];
                 load8(c, v);
     #pragma unroll
@@ -88,30 +91,31 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(int64_t rows, int co
                     hi |= ((uint32_t)quantize_one(v[4 + j], s, inv) & 0xFFu) << (8 * j);
                 }
             }
-            *reinterpret_cast<u32x2*>(q + r * ldq + c) = u32x2{lo, hi};
+            *reinterpret_cast<u32x2*>(q + r * ldq + b) = u32x2{lo, hi};
         }
     }
 }
 
 template <typename T>
-hipError_t quantize_t(int64_t rows, int cols, int ldq, const void* x, int8_t* q, float* scale, const int32_t* live,
+hipError_t quantize_t(int64_t rows, int cols, int ldq, int split, const void* x, int8_t* q, float* scale, const int32_t* live,
                       hipStream_t s) {
     const int64_t blocks = std::min<int64_t>(cols <= 2048 ? (rows + 3) / 4 : rows, 1 << 20);
     if (cols <= 2048)
-        quantize_rows_kernel<T, 64><<<(unsigned)blocks, 256, 0, s>>>(rows, cols, ldq, (const T*)x, q, scale,
+        quantize_rows_kernel<T, 64><<<(unsigned)blocks, 256, 0, s>>>(rows, cols, ldq, split, (const T*)x, q, scale,
                                                                               live);
     else
-        quantize_rows_kernel<T, 256><<<(unsigned)blocks, 256, 0, s>>>(rows, cols, ldq, (const T*)x, q, scale, live);
+        quantize_rows_kernel<T, 256><<<(unsigned)blocks, 256, 0, s>>>(rows, cols, ldq, split, (const T*)x, q, scale, live);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_quantize_rows(int64_t rows, int cols, int ldq, int dtype, const void* x, int8_t* q, float* scale,
-                                const int32_t* live, hipStream_t s) {
+hipError_t launch_quantize_rows(int64_t rows, int cols, int ldq, bool overlap, int dtype, const void* x, int8_t* q,
+                                float* scale, const int32_t* live, hipStream_t s) {
+    const int split = overlap && cols % 128 != 0 ? cols / 128 * 128 : ldq;
     timer_before(MOE_KERNEL_QUANTIZE, s);
-    const hipError_t err = dtype == MOE_DTYPE_F32 ? quantize_t<float>(rows, cols, ldq, x, q, scale, live, s)
-                                                  : quantize_t<bf16>(rows, cols, ldq, x, q, scale, live, s);
+    const hipError_t err = dtype == MOE_DTYPE_F32 ? quantize_t<float>(rows, cols, ldq, split, x, q, scale, live, s)
+                                                  : quantize_t<bf16>(rows, cols, ldq, split, x, q, scale, live, s);
     if (err == hipSuccess) timer_after(MOE_KERNEL_QUANTIZE, s);
     return err;
 }

@@ -142,10 +142,13 @@ hipError_t launch_route_backward(int T, int d, int E, int K, int dtype, int flag
                                  const float* dw, const int32_t* counts, float d_aux, float d_z, const void* dx_perm,
                                  const int32_t* assign_row, float* dl, void* dx, void* dwr, void* ws, hipStream_t s);
 // ---- 8-bit expert FFN ----------------------------------------------------------
-// Rows of q are ldq bytes long, zeros past cols; rows at or past *live (device
+// Rows of q are ldq bytes long, zeros past cols; with overlap (cols and ldq at
+// least 128, ldq a multiple of it) and cols not a multiple of 128, the row's
+// last 128 bytes instead hold the places of its last 128 columns, zeros at
+// those that the bytes before hold already.  Rows at or past *live (device
 // memory; NULL: none) are left alone.
-hipError_t launch_quantize_rows(int64_t rows, int cols, int ldq, int dtype, const void* x, int8_t* q, float* scale,
-                                const int32_t* live, hipStream_t s);
+hipError_t launch_quantize_rows(int64_t rows, int cols, int ldq, bool overlap, int dtype, const void* x, int8_t* q,
+                                float* scale, const int32_t* live, hipStream_t s);
 // n_x rows of x: the n grouped rows (rowmap NULL), or the tokens that grouped
 // row r reads as rowmap[r] / K.
 size_t ffn_i8_ws_bytes(int n_x, int n_rows, int E, int d, int F);

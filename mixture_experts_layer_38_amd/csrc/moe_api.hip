@@ -700,7 +700,7 @@ moe_status moe_quantize_rows(int64_t rows, int32_t cols, int32_t dtype, const vo
     REQUIRE(x);
     REQUIRE(q);
     REQUIRE(scale);
-    return hip_status(launch_quantize_rows(rows, cols, cols, dtype, x, q, scale, nullptr, (hipStream_t)stream));
+    return hip_status(launch_quantize_rows(rows, cols, cols, false, dtype, x, q, scale, nullptr, (hipStream_t)stream));
 }
 
 moe_status moe_expert_ffn_i8_workspace_size(const moe_problem* p, size_t* bytes) {
