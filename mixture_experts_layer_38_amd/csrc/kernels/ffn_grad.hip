@@ -1,0 +1,518 @@
+// The grouped products of the expert FFN's backward pass in bf16 (formulas:
+// ffn_train.hip).  Unlike the forward pass's, they have operands that are
+// contiguous across the reduction:
+//   GRAD_ACT  da = dh W2_e             rows [r][k] times [k][n]; epilogue: dgate, dup, act
+//   GRAD_X    dx = dgate W1_e + dup W3_e   two such products into one sum
+//   GRAD_W    dW = P^T Q               [r][m] times [r][n], the sum over the expert's rows
+//
+// Tiles of BM x 256 outputs on four waves (2 x 2), v_mfma_f32_32x32x16_bf16
+// with the n side as the first operand, so a lane ends with four consecutive
+// outputs of a row; fp32 accumulators fill the AGPRs.
+//
+// A stage is 64 wide in k.  A [k][n] operand lies in the LDS as 64 rows of 512
+// bytes and its fragments come from ds_read_b64_tr_b16, which hands each lane
+// of 16 one column of a 4 x 16 block: lane 4 r + c addresses elements
+// 4 c .. 4 c + 3 of row r, and lane i gets column i of the four rows.  Two such
+// reads give the eight k of a lane.  The 16-byte chunk c of row k is kept in
+// slot c ^ 4 (k % 4), so the 32-byte pieces of the four rows of both 16-lane
+// groups lie in distinct banks.  A [r][k] operand lies in 128-byte rows as in
+// the forward kernel (pf_swz).
+//
+// Stages go straight into the LDS with buffer loads: the descriptor carries
+// the stage's address and how many bytes of it exist, so rows past the end of
+// the group, of the reduction or of the matrix arrive as zeros and nothing
+// past an operand's last element is ever read.
+#include <algorithm>
+#include <type_traits>
+
+#include "../device_common.h"
+#include "../launch.h"
+#include "ffn_tiles.h"
+#include "gated.h"
+
+namespace moe {
+
+namespace {
+
+enum { GRAD_ACT, GRAD_X, GRAD_W };
+constexpr int GR_BN = 256;
+constexpr int GR_BK = 64;
+constexpr int GR_GM = 8;  // row tiles per group in GRAD_W's order
+
+struct GradArgs {
+    const bf16 *a0, *a1;  // rows (GRAD_X: of both products; GRAD_W: the m side of both results)
+    const bf16 *b0, *b1;  // the n side
+    bf16 *out0, *out1, *out2;
+    const bf16 *gate, *up;
+    int n_rows, E;
+    int M, N, K;  // GRAD_W: results are [M][N]; else [rows][N], K the reduction of one product
+    int lda, ldb;
+    int n_mt, n_nt, sels;  // GRAD_W: row tiles per result, results per expert
+    RowPlan plan;
+    const int32_t* offsets;
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+__device__ __forceinline__ bf16x8 read_tr(const bf16* p0, const bf16* p1) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p0);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p1);
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// KT: K is not a multiple of the stage, so a row's chunks past it are masked
+// (rows of the next one otherwise; GRAD_W has no such rows).
+template <int MODE, int BM, bool KT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void ffn_grad_kernel(GradArgs g) {
+    constexpr bool WG = MODE == GRAD_W;
+    constexpr int SA = BM * GR_BK, SB = GR_BN * GR_BK;  // elements of a stage's halves
+    constexpr int NTB = BM / 64;   // 32-wide m blocks per wave
+    constexpr int NJA = BM / 32, NJB = GR_BN / 32, NLD = NJA + NJB;  // loads per wave and stage
+    constexpr bool RING5 = BM == 256;
+    // BM 256: five 32 KB units that the halves of consecutive stages take in
+    // turn; BM 128: three whole-stage slots.
+    __shared__ __align__(1024) bf16 sA0[SA], sA1[SA], sA2[RING5 ? 1 : SA];
+    __shared__ __align__(1024) bf16 sB0[SB], sB1[SB], sB2[RING5 ? 1 : SB];
+    __shared__ __align__(1024) bf16 sU4[RING5 ? SB : 1];
+
+    const int xcd = blockIdx.x % PF_XCD, slot = blockIdx.x / PF_XCD;
+    int e, row0 = 0, row_end = 0, m0 = 0, n0, k_beg = 0, k_len = g.K;
+    const bf16 *A0 = g.a0, *A1 = g.a1, *B0 = g.b0, *B1 = g.b1;
+    bf16* out = g.out0;
+    if constexpr (WG) {
+        // every XCD takes an eighth of each result's tiles: the experts' row
+        // counts differ, the XCDs' shares of them do not
+        const int per = (g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD;
+        const int res = slot / per;
+        const int t = xcd * per + slot % per;
+        if (res >= g.E * g.sels || t >= g.n_mt * g.n_nt) return;
+        e = res / g.sels;
+        if (res % g.sels) {
+            A0 = g.a1;
+            out = g.out1;
+        }
+        const int grp = t / (GR_GM * g.n_nt), gsize = min(GR_GM, g.n_mt - grp * GR_GM);
+        const int rem = t - grp * GR_GM * g.n_nt;
+        m0 = (grp * GR_GM + rem % gsize) * BM;
+        n0 = rem / gsize * GR_BN;
+        // (in scalar registers, so that the descriptors made of them are too)
+        k_beg = __builtin_amdgcn_readfirstlane(min(max(g.offsets[e], 0), g.n_rows));
+        k_len = max(__builtin_amdgcn_readfirstlane(min(g.offsets[e + 1], g.n_rows)) - k_beg, 0);
+        out += (size_t)e * g.M * g.N;
+    } else {
+        const int n_mt = *g.plan.mt_count;
+        const int tiles = n_mt * g.n_nt;
+        const int per = (tiles + PF_XCD - 1) / PF_XCD;
+        const int t = xcd * per + slot;
+        if (slot >= per || t >= tiles) return;
+        const PfTile tl = pf_tile(t, n_mt, g.n_nt, g.plan.mt_expert, g.plan.mt_row0, g.offsets, g.n_rows);
+        e = tl.e;
+        row0 = tl.row0;
+        row_end = min(tl.row_end, row0 + BM);
+        n0 = tl.nt * GR_BN;
+        const size_t we = (size_t)e * g.K * g.N;
+        B0 += we;
+        if (MODE == GRAD_X) B1 += we;
+    }
+    const int nk1 = (k_len + GR_BK - 1) / GR_BK;  // stages of one product
+    const int nk = MODE == GRAD_X ? 2 * nk1 : nk1;
+
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int lane = lane_id();
+
+    // ---- loads -------------------------------------------------------------------
+    // [k][n] halves: instruction j of wave w fills rows 2 (w + 4 j) and the next
+    // ([k][m] with 128 m: four rows from 4 (w + 4 j)); lane p slot p % 32 (16).
+    const int brow = 2 * wave + (lane >> 5);
+    const uint32_t vb = (uint32_t)(brow * g.ldb + ((lane & 31) ^ ((brow & 3) << 2)) * 8) * 2;
+    constexpr int ACH = BM / 8;           // chunks of a [k][m] row
+    constexpr int ARI = kWave / ACH;      // rows of one instruction
+    uint32_t va[2];
+    int ac[2];
+    if constexpr (WG) {
+        const int arow = ARI * wave + lane / ACH;
+        va[0] = va[1] = (uint32_t)(arow * g.lda + ((lane % ACH) ^ ((arow & 3) << 2)) * 8) * 2;
+        ac[0] = ac[1] = 0;
+    } else {
+        // [r][k]: instruction j of wave w fills rows 8 (w + 4 j) .. + 7, whose
+        // swizzle depends on j's lowest bit
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int tr = 8 * (wave + 4 * i) + (lane >> 3);
+            ac[i] = ((lane & 7) ^ pf_swz(tr)) * 8;  // first k of the lane's chunk
+            va[i] = (uint32_t)((8 * wave + (lane >> 3)) * g.lda + ac[i]) * 2;
+        }
+    }
+    // Descriptors of stage kt: its first element and the bytes from there on that exist.
+    auto rsrc = [&](const bf16* p, int bytes) __attribute__((always_inline)) {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000);
+    };
+    auto rs_a = [&](int kt) __attribute__((always_inline)) {
+        if constexpr (WG) {
+            const int v = min(max(k_len - kt * GR_BK, 0), GR_BK);
+            return rsrc(A0 + (size_t)(k_beg + kt * GR_BK) * g.lda + m0, v > 0 ? (v * g.lda - m0) * 2 : 0);
+        } else {
+            const int seg = MODE == GRAD_X && kt >= nk1;
+            const int k0 = (kt - (seg ? nk1 : 0)) * GR_BK;
+            const int bytes = kt < nk ? ((row_end - row0) * g.lda - k0) * 2 : 0;
+            return rsrc((seg ? A1 : A0) + (size_t)row0 * g.lda + k0, bytes);
+        }
+    };
+    auto rs_b = [&](int kt) __attribute__((always_inline)) {
+        const int seg = MODE == GRAD_X && kt >= nk1;
+        const int k0 = (kt - (seg ? nk1 : 0)) * GR_BK;
+        const int v = kt < nk ? min(k_len - k0, GR_BK) : 0;
+        return rsrc((seg ? B1 : B0) + (size_t)(k_beg + k0) * g.ldb + n0, v > 0 ? (v * g.ldb - n0) * 2 : 0);
+    };
+    auto ld_a = [&](__amdgpu_buffer_rsrc_t r, int kt, int j, bf16* dst) __attribute__((always_inline)) {
+        uint32_t v = va[j & 1];
+        if constexpr (KT && !WG) {
+            const int k0 = (kt - (MODE == GRAD_X && kt >= nk1 ? nk1 : 0)) * GR_BK;
+            v = ac[j & 1] < k_len - k0 ? v : 0x80000000u;
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            r, (__attribute__((address_space(3))) void*)(dst + (wave + 4 * j) * 512), 16, v,
+            WG ? j * (4 * ARI * 2) * g.lda : j * 64 * g.lda, 0, 0);
+    };
+    auto ld_b = [&](__amdgpu_buffer_rsrc_t r, int j, bf16* dst) __attribute__((always_inline)) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            r, (__attribute__((address_space(3))) void*)(dst + (wave + 4 * j) * 512), 16, vb, j * 16 * g.ldb, 0, 0);
+    };
+
+    // ---- fragments ------------------------------------------------------------------
+    const int wm = wave & 1, wn = wave >> 1;
+    const int fhalf = lane >> 5, g16 = (lane >> 4) & 1, rr = (lane >> 2) & 3, cc = lane & 3;
+    // element offsets inside a [k][n] stage of block nb at k = 0 (k adds 256 each), and of a [k][m] one
+    int boff[4], aoff[NTB];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        boff[i] = (8 * fhalf + rr) * GR_BN + (((16 * wn + 4 * i + 2 * g16 + (cc >> 1)) ^ (rr << 2)) << 3) + (cc & 1) * 4;
+#pragma unroll
+    for (int i = 0; i < NTB; ++i) {
+        if constexpr (WG)
+            aoff[i] = (8 * fhalf + rr) * BM + (((4 * NTB * wm + 4 * i + 2 * g16 + (cc >> 1)) ^ (rr << 2)) << 3) +
+                      (cc & 1) * 4;
+        else
+            aoff[i] = (wm * (BM / 2) + i * 32 + (lane & 31)) * GR_BK;
+    }
+    int asw[NTB];
+#pragma unroll
+    for (int i = 0; i < NTB; ++i) asw[i] = pf_swz(wm * (BM / 2) + i * 32 + (lane & 31));
+    struct Frags {
+        bf16x8 n[4], m[NTB];
+    };
+    auto read = [&](const bf16* cA, const bf16* cB, int q, Frags& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f.n[i] = read_tr(cB + boff[i] + 16 * q * GR_BN, cB + boff[i] + (16 * q + 4) * GR_BN);
+#pragma unroll
+        for (int i = 0; i < NTB; ++i) {
+            if constexpr (WG)
+                f.m[i] = read_tr(cA + aoff[i] + 16 * q * BM, cA + aoff[i] + (16 * q + 4) * BM);
+            else
+                f.m[i] = *reinterpret_cast<const bf16x8*>(cA + aoff[i] + ((2 * q + fhalf) ^ asw[i]) * 8);
+        }
+    };
+    constexpr int NM = 4 * NTB;                       // MFMAs of a quarter
+    constexpr int NR = 8 + (WG ? 2 * NTB : NTB);      // LDS reads of a quarter
+    f32x16 acc[4][NTB];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < NTB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
+    auto mma = [&](const Frags& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int b = 0; b < NTB; ++b) acc[a][b] = mfma32(f.n[a], f.m[b], acc[a][b]);
+    };
+    // One quarter's schedule: reads and NV loads spread over the MFMAs.
+    auto weave = [&](auto nv_c) __attribute__((always_inline)) {
+        constexpr int NV = decltype(nv_c)::value;
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            const int nr = ((i + 1) * NR) / NM - (i * NR) / NM, nl = ((i + 1) * NV) / NM - (i * NV) / NM;
+#pragma unroll
+            for (int l = 0; l < (NR + NM - 1) / NM; ++l)
+                if (l < nr) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+            for (int l = 0; l < (NV + NM - 1) / NM; ++l)
+                if (l < nl) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+    };
+
+    // Stage kt: its four quarters, each overlapping the LDS reads of the next.
+    // After the third: this wave's reads of the stage are done and its loads of
+    // stage kt + 1 have landed; the barrier then frees the stage's units.
+    Frags fa, fb;
+    auto step5 = [&](int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA) __attribute__((always_inline)) {
+        // A(kt + 2) into pA early, B(kt + 2) into A(kt)'s unit after the barrier
+        const auto ra = rs_a(kt + 2), rb = rs_b(kt + 2);
+        read(cA, cB, 1, fb);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) ld_a(ra, kt + 2, j, pA);
+        mma(fa);
+        weave(std::integral_constant<int, 3>{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(cA, cB, 2, fa);
+#pragma unroll
+        for (int j = 3; j < 6; ++j) ld_a(ra, kt + 2, j, pA);
+        mma(fb);
+        weave(std::integral_constant<int, 3>{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(cA, cB, 3, fb);
+#pragma unroll
+        for (int j = 6; j < NJA; ++j) ld_a(ra, kt + 2, j, pA);
+        mma(fa);
+        weave(std::integral_constant<int, 2>{});
+        __builtin_amdgcn_sched_barrier(0);
+        PF_WAIT_LGKM0();
+        PF_WAIT_VM(NJA);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NJB; ++j) ld_b(rb, j, cA);
+        read(nA, nB, 0, fa);
+        mma(fb);
+        weave(std::integral_constant<int, NJB>{});
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Stage kt + 2 into slot (kt + 2) % 3, a quarter of its loads each quarter.
+    auto step3 = [&](int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA, bf16* pB) __attribute__((always_inline)) {
+        constexpr int V = NLD / 4;
+        static_assert(NLD % 4 == 0, "loads per quarter");
+        const auto ra = rs_a(kt + 2), rb = rs_b(kt + 2);
+        auto lds = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = i0; i < i0 + V; ++i) {
+                if (i < NJA) ld_a(ra, kt + 2, i, pA);
+                else ld_b(rb, i - NJA, pB);
+            }
+        };
+        read(cA, cB, 1, fb);
+        lds(0);
+        mma(fa);
+        weave(std::integral_constant<int, V>{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(cA, cB, 2, fa);
+        lds(V);
+        mma(fb);
+        weave(std::integral_constant<int, V>{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(cA, cB, 3, fb);
+        lds(2 * V);
+        mma(fa);
+        weave(std::integral_constant<int, V>{});
+        __builtin_amdgcn_sched_barrier(0);
+        PF_WAIT_LGKM0();
+        PF_WAIT_VM(3 * V);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        lds(3 * V);
+        read(nA, nB, 0, fa);
+        mma(fb);
+        weave(std::integral_constant<int, V>{});
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto first = [&](int kt, bf16* dA, bf16* dB) __attribute__((always_inline)) {
+        const auto ra = rs_a(kt), rb = rs_b(kt);
+#pragma unroll
+        for (int j = 0; j < NJA; ++j) ld_a(ra, kt, j, dA);
+#pragma unroll
+        for (int j = 0; j < NJB; ++j) ld_b(rb, j, dB);
+    };
+    if (nk > 0) {
+        if constexpr (RING5) {
+            bf16 *const u0 = sA0, *const u1 = sB0, *const u2 = sA1, *const u3 = sB1, *const u4 = sU4;
+            first(0, u0, u1);
+            first(1, u2, u3);
+            PF_WAIT_VM(NLD);
+            __builtin_amdgcn_s_barrier();
+            read(u0, u1, 0, fa);
+            const int main = nk - nk % 5;
+            for (int k = 0; k < main; k += 5) {
+                step5(k, u0, u1, u2, u3, u4);
+                step5(k + 1, u2, u3, u4, u0, u1);
+                step5(k + 2, u4, u0, u1, u2, u3);
+                step5(k + 3, u1, u2, u3, u4, u0);
+                step5(k + 4, u3, u4, u0, u1, u2);
+            }
+            const int rem = nk - main;
+            if (rem > 0) step5(main, u0, u1, u2, u3, u4);
+            if (rem > 1) step5(main + 1, u2, u3, u4, u0, u1);
+            if (rem > 2) step5(main + 2, u4, u0, u1, u2, u3);
+            if (rem > 3) step5(main + 3, u1, u2, u3, u4, u0);
+        } else {
+            first(0, sA0, sB0);
+            first(1, sA1, sB1);
+            PF_WAIT_VM(NLD);
+            __builtin_amdgcn_s_barrier();
+            read(sA0, sB0, 0, fa);
+            const int main = nk - nk % 3;
+            for (int k = 0; k < main; k += 3) {
+                step3(k, sA0, sB0, sA1, sB1, sA2, sB2);
+                step3(k + 1, sA1, sB1, sA2, sB2, sA0, sB0);
+                step3(k + 2, sA2, sB2, sA0, sB0, sA1, sB1);
+            }
+            if (nk - main > 0) step3(main, sA0, sB0, sA1, sB1, sA2, sB2);
+            if (nk - main > 1) step3(main + 1, sA1, sB1, sA2, sB2, sA0, sB0);
+        }
+    }
+    PF_WAIT_VM(0);
+    PF_WAIT_LGKM0();
+    __builtin_amdgcn_s_barrier();  // no wave reads the ring any more
+    __builtin_amdgcn_sched_barrier(0);
+
+    // ---- epilogue --------------------------------------------------------------------
+    // acc[nb][mb][i]: column wn * 128 + 32 nb + 8 (i / 4) + 4 (lane / 32) + i % 4,
+    // row wm * BM / 2 + 32 mb + lane % 32.  Each wave passes its block through an
+    // LDS unit of its own (chunks swizzled by row) and writes 16 bytes per lane.
+    bf16* const st = wave == 0 ? sB0 : wave == 1 ? sB1 : wave == 2 ? (RING5 ? sA0 : sB2) : (RING5 ? sA1 : sA0);
+    const int mrow = wm * (BM / 2), ncol = n0 + wn * 128;
+    const int el = pf_lane_fresh();
+    const int lrow = el >> 4, lch = el & 15;  // 16 chunks of eight columns per row
+    if constexpr (MODE == GRAD_ACT) {
+        // fp32 sums, 32 rows (16 KB) at a time; then gate and up by whole lines
+        float* const sf = reinterpret_cast<float*>(st);
+#pragma unroll
+        for (int mb = 0; mb < NTB; ++mb) {
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int ch = nb * 8 + 2 * q + (el >> 5), rl = el & 31;
+                    *reinterpret_cast<f32x4*>(sf + rl * 128 + ((ch ^ (rl & 7)) << 2)) =
+                        f32x4{acc[nb][mb][4 * q], acc[nb][mb][4 * q + 1], acc[nb][mb][4 * q + 2], acc[nb][mb][4 * q + 3]};
+                }
+            const int c = ncol + lch * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int rl = i * 4 + lrow, r = row0 + mrow + mb * 32 + rl;
+                const f32x4 d0 = *reinterpret_cast<const f32x4*>(sf + rl * 128 + (((2 * lch) ^ (rl & 7)) << 2));
+                const f32x4 d1 = *reinterpret_cast<const f32x4*>(sf + rl * 128 + (((2 * lch + 1) ^ (rl & 7)) << 2));
+                if (r < row_end && c < g.N) {
+                    const size_t at = (size_t)r * g.N + c;
+                    const bf16x8 gv = *reinterpret_cast<const bf16x8*>(g.gate + at);
+                    const bf16x8 uv = *reinterpret_cast<const bf16x8*>(g.up + at);
+                    bf16x8 o0, o1, o2;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const GatedGrad v = gated_grad((float)gv[j], (float)uv[j], j < 4 ? d0[j & 3] : d1[j & 3]);
+                        o0[j] = (bf16)v.dg;
+                        o1[j] = (bf16)v.du;
+                        o2[j] = (bf16)v.act;
+                    }
+                    *reinterpret_cast<bf16x8*>(g.out0 + at) = o0;
+                    *reinterpret_cast<bf16x8*>(g.out1 + at) = o1;
+                    *reinterpret_cast<bf16x8*>(g.out2 + at) = o2;
+                }
+            }
+        }
+    } else {
+        const int r_end = WG ? g.M : row_end, r0 = (WG ? m0 : row0) + mrow;
+#pragma unroll
+        for (int mb = 0; mb < NTB; ++mb) {
+            const int rl = mb * 32 + (el & 31);
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int cl = nb * 32 + 8 * q + 4 * (el >> 5);
+                    *reinterpret_cast<bf16x4*>(st + rl * 128 + (((cl >> 3) ^ (rl & 7)) << 3) + (cl & 7)) =
+                        bf16x4{(bf16)acc[nb][mb][4 * q], (bf16)acc[nb][mb][4 * q + 1], (bf16)acc[nb][mb][4 * q + 2],
+                               (bf16)acc[nb][mb][4 * q + 3]};
+                }
+        }
+        const int c = ncol + lch * 8;
+#pragma unroll
+        for (int i = 0; i < NTB * 8; ++i) {
+            const int rl = i * 4 + lrow;
+            const bf16x8 v = *reinterpret_cast<const bf16x8*>(st + rl * 128 + ((lch ^ (rl & 7)) << 3));
+            if (r0 + rl < r_end && c < g.N) *reinterpret_cast<bf16x8*>(out + (size_t)(r0 + rl) * g.N + c) = v;
+        }
+    }
+}
+
+template <int MODE, bool KT>
+hipError_t launch_grad(const GradArgs& g, int bm, unsigned grid, hipStream_t s) {
+    if (bm == 256) ffn_grad_kernel<MODE, 256, KT><<<grid, 256, 0, s>>>(g);
+    else ffn_grad_kernel<MODE, 128, KT><<<grid, 256, 0, s>>>(g);
+    return hipGetLastError();
+}
+
+// The result of P^T Q for every expert (and for a second P where a1 is given).
+hipError_t launch_grad_w(int n, int E, int M, int N, const bf16* p0, const bf16* p1, const bf16* q, bf16* out0,
+                         bf16* out1, const int32_t* offsets, hipStream_t s) {
+    GradArgs g{};
+    g.a0 = p0;
+    g.a1 = p1;
+    g.b0 = q;
+    g.out0 = out0;
+    g.out1 = out1;
+    g.n_rows = n;
+    g.E = E;
+    g.M = g.lda = M;
+    g.N = g.ldb = N;
+    g.sels = p1 != nullptr ? 2 : 1;
+    g.offsets = offsets;
+    const int bm = 256;
+    g.n_mt = (M + bm - 1) / bm;
+    g.n_nt = (N + GR_BN - 1) / GR_BN;
+    const long per = ((long)g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD;
+    return launch_grad<GRAD_W, false>(g, bm, (unsigned)(per * E * g.sels * PF_XCD), s);
+}
+
+}  // namespace
+
+hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
+                           const bf16* w3, const bf16* w2, const bf16* gate, const bf16* up, const bf16* dh, bf16* dx,
+                           bf16* dw1, bf16* dw3, bf16* dw2, bf16* dgate, bf16* dup, bf16* act, void* ws,
+                           hipStream_t s) {
+    const int bm = n >= 256 * E ? 256 : 128;
+    RowPlan plan;
+    hipError_t err = launch_row_plan(n, E, bm, offsets, ws, &plan, s);
+    if (err != hipSuccess) return err;
+    const long mt = row_plan_tiles(n, E, bm);
+    auto grid = [&](int n_nt) { return (unsigned)((mt * n_nt + PF_XCD - 1) / PF_XCD * PF_XCD); };
+    GradArgs g{};
+    g.a0 = dh;
+    g.b0 = w2;
+    g.out0 = dgate;
+    g.out1 = dup;
+    g.out2 = act;
+    g.gate = gate;
+    g.up = up;
+    g.n_rows = n;
+    g.E = E;
+    g.N = g.ldb = F;
+    g.K = g.lda = d;
+    g.n_nt = (F + GR_BN - 1) / GR_BN;
+    g.plan = plan;
+    g.offsets = offsets;
+    err = d % GR_BK == 0 ? launch_grad<GRAD_ACT, false>(g, bm, grid(g.n_nt), s)
+                         : launch_grad<GRAD_ACT, true>(g, bm, grid(g.n_nt), s);
+    if (err != hipSuccess) return err;
+    if (dw2 != nullptr) {
+        if ((err = launch_grad_w(n, E, d, F, dh, nullptr, act, dw2, nullptr, offsets, s)) != hipSuccess) return err;
+        if ((err = launch_grad_w(n, E, F, d, dgate, dup, x, dw1, dw3, offsets, s)) != hipSuccess) return err;
+    }
+    if (dx != nullptr) {
+        g.a0 = dgate;
+        g.a1 = dup;
+        g.b0 = w1;
+        g.b1 = w3;
+        g.out0 = dx;
+        g.N = g.ldb = d;
+        g.K = g.lda = F;
+        g.n_nt = (d + GR_BN - 1) / GR_BN;
+        err = F % GR_BK == 0 ? launch_grad<GRAD_X, false>(g, bm, grid(g.n_nt), s)
+                             : launch_grad<GRAD_X, true>(g, bm, grid(g.n_nt), s);
+    }
+    return err;
+}
+
+}  // namespace moe

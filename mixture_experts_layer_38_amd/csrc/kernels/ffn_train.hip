@@ -18,6 +18,11 @@ hipError_t launch_ffn_prefill_keep(int n_rows, int E, int d, int F, const bf16* 
                                    const bf16* w1, const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act,
                                    bf16* h, void* ws, hipStream_t s);
 
+hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
+                           const bf16* w3, const bf16* w2, const bf16* gate, const bf16* up, const bf16* dh, bf16* dx,
+                           bf16* dw1, bf16* dw3, bf16* dw2, bf16* dgate, bf16* dup, bf16* act, void* ws,
+                           hipStream_t s);
+
 namespace {
 
 // ---- fp32 path -------------------------------------------------------------------
@@ -85,10 +90,11 @@ hipError_t train_gemms(int n, int E, int d, int F, const float* x, const int32_t
     return hipGetLastError();
 }
 
-template <typename T>
-hipError_t backward_gemms(int n, int E, int d, int F, const T* x, const int32_t* offsets, const T* w1, const T* w3,
-                          const T* w2, const T* gate, const T* up, const T* dh, T* dx, T* dw1, T* dw3, T* dw2,
-                          T* dgate, T* dup, T* act, const RowPlan& plan, hipStream_t s) {
+hipError_t backward_gemms(int n, int E, int d, int F, const float* x, const int32_t* offsets, const float* w1,
+                          const float* w3, const float* w2, const float* gate, const float* up, const float* dh,
+                          float* dx, float* dw1, float* dw3, float* dw2, float* dgate, float* dup, float* act,
+                          const RowPlan& plan, hipStream_t s) {
+    typedef float T;
     const unsigned mt = (unsigned)row_plan_tiles(n, E, GM_T);
     const unsigned td = (d + GM_T - 1) / GM_T, tf = (F + GM_T - 1) / GM_T;
     const size_t ws = (size_t)F * d;
@@ -158,20 +164,20 @@ hipError_t launch_ffn_backward(int T, int K, int E, int d, int F, int dtype, con
     const size_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
     const size_t one = align_up((size_t)n * F * es, 256);
     char* base = (char*)ws;
-    RowPlan plan;
+    void *dgate = base, *dup = base + one, *act = base + 2 * one, *rest = base + 3 * one;
+    hipError_t err;
     timer_before(MOE_KERNEL_FFN_BACKWARD, s);
-    hipError_t err = launch_row_plan(n, E, GM_T, offsets, base + 3 * one, &plan, s);
-    if (err != hipSuccess) return err;
-    if (dtype == MOE_DTYPE_F32)
-        err = backward_gemms<float>(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3,
-                                     (const float*)w2, (const float*)gate, (const float*)up, (const float*)dh,
-                                     (float*)dx, (float*)dw1, (float*)dw3, (float*)dw2, (float*)base,
-                                     (float*)(base + one), (float*)(base + 2 * one), plan, s);
-    else
-        err = backward_gemms<bf16>(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3,
-                                   (const bf16*)w2, (const bf16*)gate, (const bf16*)up, (const bf16*)dh, (bf16*)dx,
-                                   (bf16*)dw1, (bf16*)dw3, (bf16*)dw2, (bf16*)base, (bf16*)(base + one),
-                                   (bf16*)(base + 2 * one), plan, s);
+    if (dtype == MOE_DTYPE_F32) {
+        RowPlan plan;
+        if ((err = launch_row_plan(n, E, GM_T, offsets, rest, &plan, s)) != hipSuccess) return err;
+        err = backward_gemms(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3,
+                             (const float*)w2, (const float*)gate, (const float*)up, (const float*)dh, (float*)dx,
+                             (float*)dw1, (float*)dw3, (float*)dw2, (float*)dgate, (float*)dup, (float*)act, plan, s);
+    } else {
+        err = launch_ffn_grad(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3, (const bf16*)w2,
+                              (const bf16*)gate, (const bf16*)up, (const bf16*)dh, (bf16*)dx, (bf16*)dw1, (bf16*)dw3,
+                              (bf16*)dw2, (bf16*)dgate, (bf16*)dup, (bf16*)act, rest, s);
+    }
     if (err == hipSuccess) timer_after(MOE_KERNEL_FFN_BACKWARD, s);
     return err;
 }
