@@ -87,16 +87,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         const int res = slot / per;
         const int t = xcd * per + slot % per;
         if (res >= g.E * g.sels || t >= g.n_mt * g.n_nt) return;
-        e = res / g.sels;
-        if (res % g.sels) {
+        // Uniform values are put into scalar registers (the divisions ran in
+        // vector ones), so that the descriptors made of them are scalar too.
+        e = __builtin_amdgcn_readfirstlane(res / g.sels);
+        if (__builtin_amdgcn_readfirstlane(res % g.sels)) {
             A0 = g.a1;
             out = g.out1;
         }
         const int grp = t / (GR_GM * g.n_nt), gsize = min(GR_GM, g.n_mt - grp * GR_GM);
         const int rem = t - grp * GR_GM * g.n_nt;
-        m0 = (grp * GR_GM + rem % gsize) * BM;
-        n0 = rem / gsize * GR_BN;
-        // (in scalar registers, so that the descriptors made of them are too)
+        m0 = __builtin_amdgcn_readfirstlane((grp * GR_GM + rem % gsize) * BM);
+        n0 = __builtin_amdgcn_readfirstlane(rem / gsize * GR_BN);
         k_beg = __builtin_amdgcn_readfirstlane(min(max(g.offsets[e], 0), g.n_rows));
         k_len = max(__builtin_amdgcn_readfirstlane(min(g.offsets[e + 1], g.n_rows)) - k_beg, 0);
         out += (size_t)e * g.M * g.N;
