@@ -36,7 +36,7 @@ namespace {
 
 enum { GRAD_ACT, GRAD_X, GRAD_W };
 constexpr int GR_BN = 256;
-constexpr int GR_BK = 64;
+constexpr int GR_W_LONG = 512;
 constexpr int GR_GM = 8;  // row tiles per group in GRAD_W's order
 
 struct GradArgs {
@@ -64,14 +64,16 @@ __device__ __forceinline__ bf16x8 read_tr(const bf16* p0, const bf16* p1) {
 // KT: K is not a multiple of the stage, so a row's chunks past it are masked
 // (rows of the next one otherwise; GRAD_W has no such rows).
 template <int MODE, int BM, bool KT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void ffn_grad_kernel(GradArgs g) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == 256 ? 1 : 2, BM == 256 ? 1 : 2)))
+void ffn_grad_kernel(GradArgs g) {
     constexpr bool WG = MODE == GRAD_W;
+    constexpr int GR_BK = BM == 256 ? 64 : 32;  // k per stage
     constexpr int SA = BM * GR_BK, SB = GR_BN * GR_BK;  // elements of a stage's halves
     constexpr int NTB = BM / 64;   // 32-wide m blocks per wave
-    constexpr int NJA = BM / 32, NJB = GR_BN / 32, NLD = NJA + NJB;  // loads per wave and stage
+    constexpr int NJA = SA / 2048, NJB = SB / 2048, NLD = NJA + NJB;  // loads per wave and stage
     constexpr bool RING5 = BM == 256;
     // BM 256: five 32 KB units that the halves of consecutive stages take in
-    // turn; BM 128: three whole-stage slots.
+    // turn; BM 128: three slots of 24 KB for whole stages (two workgroups per CU).
     __shared__ __align__(1024) bf16 sA0[SA], sA1[SA], sA2[RING5 ? 1 : SA];
     __shared__ __align__(1024) bf16 sB0[SB], sB1[SB], sB2[RING5 ? 1 : SB];
     __shared__ __align__(1024) bf16 sU4[RING5 ? SB : 1];
@@ -135,9 +137,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         const int arow = ARI * wave + lane / ACH;
         va[0] = va[1] = (uint32_t)(arow * g.lda + ((lane % ACH) ^ ((arow & 3) << 2)) * 8) * 2;
         ac[0] = ac[1] = 0;
+    } else if constexpr (GR_BK == 32) {
+        // [r][k] of 64-byte rows: instruction j of wave w fills rows 16 (w + 4 j) .. + 15
+        ac[0] = ac[1] = ((lane & 3) ^ ((lane >> 3) & 3)) * 8;
+        va[0] = va[1] = (uint32_t)((16 * wave + (lane >> 2)) * g.lda + ac[0]) * 2;
     } else {
-        // [r][k]: instruction j of wave w fills rows 8 (w + 4 j) .. + 7, whose
-        // swizzle depends on j's lowest bit
+        // [r][k] of 128-byte rows: instruction j of wave w fills rows
+        // 8 (w + 4 j) .. + 7, whose swizzle depends on j's lowest bit
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int tr = 8 * (wave + 4 * i) + (lane >> 3);
@@ -174,7 +180,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         }
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             r, (__attribute__((address_space(3))) void*)(dst + (wave + 4 * j) * 512), 16, v,
-            WG ? j * (4 * ARI * 2) * g.lda : j * 64 * g.lda, 0, 0);
+            WG ? j * (4 * ARI * 2) * g.lda : j * (4096 / GR_BK) * g.lda, 0, 0);
     };
     auto ld_b = [&](__amdgpu_buffer_rsrc_t r, int j, bf16* dst) __attribute__((always_inline)) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -199,7 +205,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     }
     int asw[NTB];
 #pragma unroll
-    for (int i = 0; i < NTB; ++i) asw[i] = pf_swz(wm * (BM / 2) + i * 32 + (lane & 31));
+    for (int i = 0; i < NTB; ++i) {
+        const int r = wm * (BM / 2) + i * 32 + (lane & 31);
+        asw[i] = GR_BK == 32 ? (r >> 1) & 3 : pf_swz(r);
+    }
     struct Frags {
         bf16x8 n[4], m[NTB];
     };
@@ -282,10 +291,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         weave(std::integral_constant<int, NJB>{});
         __builtin_amdgcn_sched_barrier(0);
     };
-    // Stage kt + 2 into slot (kt + 2) % 3, a quarter of its loads each quarter.
+    // Stage kt + 2 into slot (kt + 2) % 3, half of its loads in each of the
+    // stage's two 16-wide parts.
     auto step3 = [&](int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA, bf16* pB) __attribute__((always_inline)) {
-        constexpr int V = NLD / 4;
-        static_assert(NLD % 4 == 0, "loads per quarter");
+        constexpr int V = NLD / 2;
         const auto ra = rs_a(kt + 2), rb = rs_b(kt + 2);
         auto lds = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
@@ -299,21 +308,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         mma(fa);
         weave(std::integral_constant<int, V>{});
         __builtin_amdgcn_sched_barrier(0);
-        read(cA, cB, 2, fa);
-        lds(V);
-        mma(fb);
-        weave(std::integral_constant<int, V>{});
-        __builtin_amdgcn_sched_barrier(0);
-        read(cA, cB, 3, fb);
-        lds(2 * V);
-        mma(fa);
-        weave(std::integral_constant<int, V>{});
-        __builtin_amdgcn_sched_barrier(0);
         PF_WAIT_LGKM0();
-        PF_WAIT_VM(3 * V);
+        PF_WAIT_VM(V);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        lds(3 * V);
+        lds(V);
         read(nA, nB, 0, fa);
         mma(fb);
         weave(std::integral_constant<int, V>{});
@@ -372,68 +371,78 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // acc[nb][mb][i]: column wn * 128 + 32 nb + 8 (i / 4) + 4 (lane / 32) + i % 4,
     // row wm * BM / 2 + 32 mb + lane % 32.  Each wave passes its block through an
     // LDS unit of its own (chunks swizzled by row) and writes 16 bytes per lane.
-    bf16* const st = wave == 0 ? sB0 : wave == 1 ? sB1 : wave == 2 ? (RING5 ? sA0 : sB2) : (RING5 ? sA1 : sA0);
+    bf16* const st = RING5 ? (wave == 0 ? sB0 : wave == 1 ? sB1 : wave == 2 ? sA0 : sA1)
+                           : (wave == 0 ? sB0 : wave == 1 ? sB1 : wave == 2 ? sB2 : sA0);
     const int mrow = wm * (BM / 2), ncol = n0 + wn * 128;
     const int el = pf_lane_fresh();
-    const int lrow = el >> 4, lch = el & 15;  // 16 chunks of eight columns per row
     if constexpr (MODE == GRAD_ACT) {
-        // fp32 sums, 32 rows (16 KB) at a time; then gate and up by whole lines
+        // fp32 sums, 32 rows x 64 columns (8 KB) at a time; then gate and up by whole lines
         float* const sf = reinterpret_cast<float*>(st);
+        const int lrow = el >> 3, lch = el & 7;  // eight chunks of eight columns per row
 #pragma unroll
-        for (int mb = 0; mb < NTB; ++mb) {
+        for (int mb = 0; mb < NTB; ++mb)
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb)
+            for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int ch = nb * 8 + 2 * q + (el >> 5), rl = el & 31;
-                    *reinterpret_cast<f32x4*>(sf + rl * 128 + ((ch ^ (rl & 7)) << 2)) =
-                        f32x4{acc[nb][mb][4 * q], acc[nb][mb][4 * q + 1], acc[nb][mb][4 * q + 2], acc[nb][mb][4 * q + 3]};
-                }
-            const int c = ncol + lch * 8;
+                for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int rl = i * 4 + lrow, r = row0 + mrow + mb * 32 + rl;
-                const f32x4 d0 = *reinterpret_cast<const f32x4*>(sf + rl * 128 + (((2 * lch) ^ (rl & 7)) << 2));
-                const f32x4 d1 = *reinterpret_cast<const f32x4*>(sf + rl * 128 + (((2 * lch + 1) ^ (rl & 7)) << 2));
-                if (r < row_end && c < g.N) {
-                    const size_t at = (size_t)r * g.N + c;
-                    const bf16x8 gv = *reinterpret_cast<const bf16x8*>(g.gate + at);
-                    const bf16x8 uv = *reinterpret_cast<const bf16x8*>(g.up + at);
-                    bf16x8 o0, o1, o2;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const GatedGrad v = gated_grad((float)gv[j], (float)uv[j], j < 4 ? d0[j & 3] : d1[j & 3]);
-                        o0[j] = (bf16)v.dg;
-                        o1[j] = (bf16)v.du;
-                        o2[j] = (bf16)v.act;
+                    for (int q = 0; q < 4; ++q) {
+                        const int ch = nb * 8 + 2 * q + (el >> 5), rl = el & 31;
+                        const f32x16& a = acc[2 * half + nb][mb];
+                        *reinterpret_cast<f32x4*>(sf + rl * 64 + ((ch ^ (rl & 15)) << 2)) =
+                            f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
                     }
-                    *reinterpret_cast<bf16x8*>(g.out0 + at) = o0;
-                    *reinterpret_cast<bf16x8*>(g.out1 + at) = o1;
-                    *reinterpret_cast<bf16x8*>(g.out2 + at) = o2;
+                const int c = ncol + half * 64 + lch * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rl = i * 8 + lrow, r = row0 + mrow + mb * 32 + rl;
+                    const f32x4 d0 = *reinterpret_cast<const f32x4*>(sf + rl * 64 + (((2 * lch) ^ (rl & 15)) << 2));
+                    const f32x4 d1 = *reinterpret_cast<const f32x4*>(sf + rl * 64 + (((2 * lch + 1) ^ (rl & 15)) << 2));
+                    if (r < row_end && c < g.N) {
+                        const size_t at = (size_t)r * g.N + c;
+                        const bf16x8 gv = *reinterpret_cast<const bf16x8*>(g.gate + at);
+                        const bf16x8 uv = *reinterpret_cast<const bf16x8*>(g.up + at);
+                        bf16x8 o0, o1, o2;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const GatedGrad v = gated_grad((float)gv[j], (float)uv[j], j < 4 ? d0[j & 3] : d1[j & 3]);
+                            o0[j] = (bf16)v.dg;
+                            o1[j] = (bf16)v.du;
+                            o2[j] = (bf16)v.act;
+                        }
+                        *reinterpret_cast<bf16x8*>(g.out0 + at) = o0;
+                        *reinterpret_cast<bf16x8*>(g.out1 + at) = o1;
+                        *reinterpret_cast<bf16x8*>(g.out2 + at) = o2;
+                    }
                 }
             }
-        }
     } else {
+        // in passes of the rows that a unit holds
+        constexpr int PB = RING5 ? NTB : 1;  // 32-row blocks per pass
+        const int lrow = el >> 4, lch = el & 15;  // 16 chunks of eight columns per row
         const int r_end = WG ? g.M : row_end, r0 = (WG ? m0 : row0) + mrow;
-#pragma unroll
-        for (int mb = 0; mb < NTB; ++mb) {
-            const int rl = mb * 32 + (el & 31);
-#pragma unroll
-            for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int cl = nb * 32 + 8 * q + 4 * (el >> 5);
-                    *reinterpret_cast<bf16x4*>(st + rl * 128 + (((cl >> 3) ^ (rl & 7)) << 3) + (cl & 7)) =
-                        bf16x4{(bf16)acc[nb][mb][4 * q], (bf16)acc[nb][mb][4 * q + 1], (bf16)acc[nb][mb][4 * q + 2],
-                               (bf16)acc[nb][mb][4 * q + 3]};
-                }
-        }
         const int c = ncol + lch * 8;
 #pragma unroll
-        for (int i = 0; i < NTB * 8; ++i) {
-            const int rl = i * 4 + lrow;
-            const bf16x8 v = *reinterpret_cast<const bf16x8*>(st + rl * 128 + ((lch ^ (rl & 7)) << 3));
-            if (r0 + rl < r_end && c < g.N) *reinterpret_cast<bf16x8*>(out + (size_t)(r0 + rl) * g.N + c) = v;
+        for (int p = 0; p < NTB; p += PB) {
+#pragma unroll
+            for (int mb = p; mb < p + PB; ++mb) {
+                const int rl = (mb - p) * 32 + (el & 31);
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int cl = nb * 32 + 8 * q + 4 * (el >> 5);
+                        *reinterpret_cast<bf16x4*>(st + rl * 128 + (((cl >> 3) ^ (rl & 7)) << 3) + (cl & 7)) =
+                            bf16x4{(bf16)acc[nb][mb][4 * q], (bf16)acc[nb][mb][4 * q + 1], (bf16)acc[nb][mb][4 * q + 2],
+                                   (bf16)acc[nb][mb][4 * q + 3]};
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < PB * 8; ++i) {
+                const int rl = i * 4 + lrow, r = r0 + p * 32 + rl;
+                const bf16x8 v = *reinterpret_cast<const bf16x8*>(st + rl * 128 + ((lch ^ (rl & 7)) << 3));
+                if (r < r_end && c < g.N) *reinterpret_cast<bf16x8*>(out + (size_t)r * g.N + c) = v;
+            }
         }
     }
 }
@@ -460,7 +469,7 @@ hipError_t launch_grad_w(int n, int E, int M, int N, const bf16* p0, const bf16*
     g.N = g.ldb = N;
     g.sels = p1 != nullptr ? 2 : 1;
     g.offsets = offsets;
-    const int bm = 256;
+    const int bm = n >= GR_W_LONG * E ? 256 : 128;
     g.n_mt = (M + bm - 1) / bm;
     g.n_nt = (N + GR_BN - 1) / GR_BN;
     const long per = ((long)g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD;
@@ -473,7 +482,7 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
                            const bf16* w3, const bf16* w2, const bf16* gate, const bf16* up, const bf16* dh, bf16* dx,
                            bf16* dw1, bf16* dw3, bf16* dw2, bf16* dgate, bf16* dup, bf16* act, void* ws,
                            hipStream_t s) {
-    const int bm = n >= 256 * E ? 256 : 128;
+    const int bm = n >= 128 * E ? 256 : 128;
     RowPlan plan;
     hipError_t err = launch_row_plan(n, E, bm, offsets, ws, &plan, s);
     if (err != hipSuccess) return err;
@@ -494,7 +503,7 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
     g.n_nt = (F + GR_BN - 1) / GR_BN;
     g.plan = plan;
     g.offsets = offsets;
-    err = d % GR_BK == 0 ? launch_grad<GRAD_ACT, false>(g, bm, grid(g.n_nt), s)
+    err = d % 64 == 0 ? launch_grad<GRAD_ACT, false>(g, bm, grid(g.n_nt), s)
                          : launch_grad<GRAD_ACT, true>(g, bm, grid(g.n_nt), s);
     if (err != hipSuccess) return err;
     if (dw2 != nullptr) {
@@ -510,7 +519,7 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
         g.N = g.ldb = d;
         g.K = g.lda = F;
         g.n_nt = (d + GR_BN - 1) / GR_BN;
-        err = F % GR_BK == 0 ? launch_grad<GRAD_X, false>(g, bm, grid(g.n_nt), s)
+        err = F % 64 == 0 ? launch_grad<GRAD_X, false>(g, bm, grid(g.n_nt), s)
                              : launch_grad<GRAD_X, true>(g, bm, grid(g.n_nt), s);
     }
     return err;
