@@ -379,43 +379,53 @@ void ffn_grad_kernel(GradArgs g) {
         // fp32 sums, 32 rows x 64 columns (8 KB) at a time; then gate and up by whole lines
         float* const sf = reinterpret_cast<float*>(st);
         const int lrow = el >> 3, lch = el & 7;  // eight chunks of eight columns per row
+        bf16x8 gv[2][4], uv[2][4];  // a pass's gate and up, loaded one pass ahead
+        auto fetch = [&](int p) __attribute__((always_inline)) {
+            const int c = min(ncol + (p & 1) * 64 + lch * 8, g.N - 8);
 #pragma unroll
-        for (int mb = 0; mb < NTB; ++mb)
+            for (int i = 0; i < 4; ++i) {
+                const int r = min(row0 + mrow + (p >> 1) * 32 + i * 8 + lrow, row_end - 1);
+                gv[p & 1][i] = *reinterpret_cast<const bf16x8*>(g.gate + (size_t)r * g.N + c);
+                uv[p & 1][i] = *reinterpret_cast<const bf16x8*>(g.up + (size_t)r * g.N + c);
+            }
+        };
+        fetch(0);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+        for (int p = 0; p < 2 * NTB; ++p) {
+            const int mb = p >> 1, half = p & 1;
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
+            for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int ch = nb * 8 + 2 * q + (el >> 5), rl = el & 31;
-                        const f32x16& a = acc[2 * half + nb][mb];
-                        *reinterpret_cast<f32x4*>(sf + rl * 64 + ((ch ^ (rl & 15)) << 2)) =
-                            f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
-                    }
-                const int c = ncol + half * 64 + lch * 8;
+                for (int q = 0; q < 4; ++q) {
+                    const int ch = nb * 8 + 2 * q + (el >> 5), rl = el & 31;
+                    const f32x16& a = acc[2 * half + nb][mb];
+                    *reinterpret_cast<f32x4*>(sf + rl * 64 + ((ch ^ (rl & 15)) << 2)) =
+                        f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+                }
+            if (p + 1 < 2 * NTB) fetch(p + 1);
+            const int c = ncol + half * 64 + lch * 8;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int rl = i * 8 + lrow, r = row0 + mrow + mb * 32 + rl;
-                    const f32x4 d0 = *reinterpret_cast<const f32x4*>(sf + rl * 64 + (((2 * lch) ^ (rl & 15)) << 2));
-                    const f32x4 d1 = *reinterpret_cast<const f32x4*>(sf + rl * 64 + (((2 * lch + 1) ^ (rl & 15)) << 2));
-                    if (r < row_end && c < g.N) {
-                        const size_t at = (size_t)r * g.N + c;
-                        const bf16x8 gv = *reinterpret_cast<const bf16x8*>(g.gate + at);
-                        const bf16x8 uv = *reinterpret_cast<const bf16x8*>(g.up + at);
-                        bf16x8 o0, o1, o2;
+            for (int i = 0; i < 4; ++i) {
+                const int rl = i * 8 + lrow, r = row0 + mrow + mb * 32 + rl;
+                const f32x4 d0 = *reinterpret_cast<const f32x4*>(sf + rl * 64 + (((2 * lch) ^ (rl & 15)) << 2));
+                const f32x4 d1 = *reinterpret_cast<const f32x4*>(sf + rl * 64 + (((2 * lch + 1) ^ (rl & 15)) << 2));
+                bf16x8 o0, o1, o2;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const GatedGrad v = gated_grad((float)gv[j], (float)uv[j], j < 4 ? d0[j & 3] : d1[j & 3]);
-                            o0[j] = (bf16)v.dg;
-                            o1[j] = (bf16)v.du;
-                            o2[j] = (bf16)v.act;
-                        }
-                        *reinterpret_cast<bf16x8*>(g.out0 + at) = o0;
-                        *reinterpret_cast<bf16x8*>(g.out1 + at) = o1;
-                        *reinterpret_cast<bf16x8*>(g.out2 + at) = o2;
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    const GatedGrad v =
+                        gated_grad((float)gv[p & 1][i][j], (float)uv[p & 1][i][j], j < 4 ? d0[j & 3] : d1[j & 3]);
+                    o0[j] = (bf16)v.dg;
+                    o1[j] = (bf16)v.du;
+                    o2[j] = (bf16)v.act;
+                }
+                if (r < row_end && c < g.N) {
+                    const size_t at = (size_t)r * g.N + c;
+                    *reinterpret_cast<bf16x8*>(g.out0 + at) = o0;
+                    *reinterpret_cast<bf16x8*>(g.out1 + at) = o1;
+                    *reinterpret_cast<bf16x8*>(g.out2 + at) = o2;
                 }
             }
+        }
     } else {
         // in passes of the rows that a unit holds
         constexpr int PB = RING5 ? NTB : 1;  // 32-row blocks per pass
