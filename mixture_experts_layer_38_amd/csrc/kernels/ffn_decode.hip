@@ -21,6 +21,7 @@
 
 #include "../device_common.h"
 #include "../launch.h"
+#include "ffn_tiles.h"
 
 namespace moe {
 
@@ -46,15 +47,20 @@ __device__ __forceinline__ u32x4 load16_masked(const bf16* row, int k, int K) {
 // from A row rowmap[r * topk] as is, or as zeros when that entry is negative
 // (the slots of a concatenation); otherwise row r is A row
 // rowmap[r] / topk (rowmap NULL: row r).
-template <bool GATED, int CPI, int NCB, bool ALIGNED, int R, bool PART = false, bool ZNEG = false>
+// With PfScales the rows hold 8-bit integers, two to a unit of K, lda and ldw:
+// the same loads feed v_mfma_i32_16x16x64_i8, and the epilogue scales the sums.
+template <bool GATED, int CPI, int NCB, bool ALIGNED, int R, bool PART = false, bool ZNEG = false, typename... X>
 __device__ __forceinline__ void ffn_decode_group(
     int e, int n_rows, int N, int K, const bf16* __restrict__ A, const int32_t* __restrict__ rowmap, int topk,
     const int32_t* __restrict__ offsets, const bf16* __restrict__ Wa, const bf16* __restrict__ Wb,
-    bf16* __restrict__ out, int lda, int ldw, float* __restrict__ part = nullptr) {
+    bf16* __restrict__ out, int lda, int ldw, float* __restrict__ part = nullptr, X... extra) {
+    constexpr bool I8 = pf_int8<X...>;
+    typedef typename std::conditional<I8, i32x4, f32x4>::type Acc;
+    typedef typename std::conditional<I8, int32_t, float>::type Sum;
     constexpr int NG = GATED ? 2 : 1;
     constexpr int NS = 4 * CPI;          // 32-wide slices per chunk
     constexpr int KCH = DC_KCH * CPI;  // k per chunk
-    __shared__ float red[DC_WAVES - 1][R][NCB][NG][4][kWave];
+    __shared__ Sum red[DC_WAVES - 1][R][NCB][NG][4][kWave];
     const int n0 = blockIdx.x * DC_ROWS * R;
     const int r0 = offsets ? offsets[e] : 0;
     const int m = (offsets ? min(offsets[e + 1], n_rows) : n_rows) - r0;
@@ -81,13 +87,13 @@ __device__ __forceinline__ void ffn_decode_group(
     for (int p0 = 0; p0 < m; p0 += 16 * NCB) {
         const int mp = min(m - p0, 16 * NCB);
         const int ncb = (mp + 15) / 16;
-        f32x4 acc[R][NCB][NG];
+        Acc acc[R][NCB][NG];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int cb = 0; cb < NCB; ++cb)
 #pragma unroll
-                for (int gi = 0; gi < NG; ++gi) acc[r][cb][gi] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int gi = 0; gi < NG; ++gi) acc[r][cb][gi] = Acc{0, 0, 0, 0};
         const bf16* arow[NCB];
         bool azero[NCB];
 #pragma unroll
@@ -148,9 +154,14 @@ __device__ __forceinline__ void ffn_decode_group(
                         const bf16x8 xb = as_bf16x8(xv[cb][s]);
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
-                            acc[r][cb][0] = mfma16(as_bf16x8(wc[r][0][s]), xb, acc[r][cb][0]);
-                            if (GATED)
-                                acc[r][cb][NG - 1] = mfma16(as_bf16x8(wc[r][NG - 1][s]), xb, acc[r][cb][NG - 1]);
+                            if constexpr (I8) {
+                                acc[r][cb][0] = mfma16_i8(wc[r][0][s], xv[cb][s], acc[r][cb][0]);
+                                if (GATED) acc[r][cb][NG - 1] = mfma16_i8(wc[r][NG - 1][s], xv[cb][s], acc[r][cb][NG - 1]);
+                            } else {
+                                acc[r][cb][0] = mfma16(as_bf16x8(wc[r][0][s]), xb, acc[r][cb][0]);
+                                if (GATED)
+                                    acc[r][cb][NG - 1] = mfma16(as_bf16x8(wc[r][NG - 1][s]), xb, acc[r][cb][NG - 1]);
+                            }
                         }
                     }
                 }
@@ -182,16 +193,30 @@ __device__ __forceinline__ void ffn_decode_group(
                     // lane holds output (weight row 4g + i of block r, token column rl)
                     const int tcol = cb * 16 + rl;
                     float v[4];
+                    float rs = 0.0f;
+                    f32x4 wsa, wsb;
+                    if constexpr (I8) {  // N is a multiple of 16
+                        const PfScales sc = pf_extra<PfScales>(extra...);
+                        rs = sc.rows[src_row(rowmap, topk, r0 + p0 + min(tcol, mp - 1))];
+                        const size_t at = (size_t)e * N + min(n0 + DC_ROWS * r + g * 4, N - 4);
+                        wsa = *reinterpret_cast<const f32x4*>(sc.wa + at);
+                        if (GATED) wsb = *reinterpret_cast<const f32x4*>(sc.wb + at);
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float s0 = acc[r][cb][0][i];
-                        float s1 = GATED ? acc[r][cb][NG - 1][i] : 0.0f;
+                        Sum s0 = acc[r][cb][0][i];
+                        Sum s1 = GATED ? acc[r][cb][NG - 1][i] : 0;
 #pragma unroll
                         for (int w = 0; w < DC_WAVES - 1; ++w) {
                             s0 += red[w][r][cb][0][i][lane];
                             if (GATED) s1 += red[w][r][cb][NG - 1][i][lane];
                         }
-                        v[i] = GATED ? silu(s0) * s1 : s0;
+                        if constexpr (I8) {
+                            const float f0 = (float)s0 * rs * wsa[i];
+                            v[i] = GATED ? silu(f0) * ((float)s1 * rs * wsb[i]) : f0;
+                        } else {
+                            v[i] = GATED ? silu(s0) * s1 : s0;
+                        }
                     }
                     if (PART && tcol < mp) {
                         // N is a multiple of 4 here (the caller checks), so
@@ -247,6 +272,28 @@ __global__ __launch_bounds__(DC_WAVES * kWave) void ffn_decode_expert_kernel(
         ffn_decode_group<GATED, CPI2, 2, ALIGNED, R>(e, n_rows, N, K, A, rowmap, topk, offsets, Wa, Wb, out, K, K);
     else
         ffn_decode_group<GATED, 1, 4, ALIGNED, R>(e, n_rows, N, K, A, rowmap, topk, offsets, Wa, Wb, out, K, K);
+}
+
+// The same on 8-bit rows and weights (K: units of two values; rows of A padded
+// to whole 128-byte lines).
+template <bool GATED, int CPI1, int CPI2, bool ALIGNED, int R, bool FOUR, int WPE>
+__global__ __launch_bounds__(DC_WAVES * kWave) __attribute__((amdgpu_waves_per_eu(WPE)))
+void ffn_decode_i8_kernel(
+    int n_rows, int N, int K, const bf16* __restrict__ A, const int32_t* __restrict__ rowmap, int topk,
+    const int32_t* __restrict__ offsets, const bf16* __restrict__ Wa, const bf16* __restrict__ Wb,
+    bf16* __restrict__ out, PfScales scales) {
+    const int e = blockIdx.y;
+    const int m = min(offsets[e + 1], n_rows) - offsets[e];
+    const int lda = (K + 63) / 64 * 64;
+    if (m <= DC_ROWS)
+        ffn_decode_group<GATED, CPI1, 1, ALIGNED, R, false, false, PfScales>(e, n_rows, N, K, A, rowmap, topk, offsets,
+                                                                             Wa, Wb, out, lda, K, nullptr, scales);
+    else if (!FOUR || m <= 2 * DC_ROWS)
+        ffn_decode_group<GATED, CPI2, 2, ALIGNED, R, false, false, PfScales>(e, n_rows, N, K, A, rowmap, topk, offsets,
+                                                                             Wa, Wb, out, lda, K, nullptr, scales);
+    else
+        ffn_decode_group<GATED, 1, 4, ALIGNED, R, false, false, PfScales>(e, n_rows, N, K, A, rowmap, topk, offsets, Wa,
+                                                                          Wb, out, lda, K, nullptr, scales);
 }
 
 // The experts listed in elist[0 .. *ecount) (small groups of a large batch),
@@ -514,6 +561,34 @@ hipError_t launch_concat_small(int T, int Ks, int d, const void* h, const int32_
     const int n = T * d;
     linear_part_reduce_kernel<<<std::max(1, std::min((n + 255) / 256, 1024)), 256, 0, s>>>(n, parts, part,
                                                                                           (bf16*)y);
+    return hipGetLastError();
+}
+
+// One GEMM of a decode-sized batch on 8-bit weights (K: values): the kernels
+// and strip shapes of launch_decode_t.
+hipError_t launch_decode_i8(bool gated, int n_rows, int E, int N, int K, const int8_t* A, const float* rows,
+                            const int32_t* rowmap, int topk, const int32_t* offsets, const int8_t* wa, const float* sa,
+                            const int8_t* wb, const float* sb, bf16* out, hipStream_t s) {
+    const bf16 *a = (const bf16*)A, *w0 = (const bf16*)wa, *w1 = (const bf16*)wb;
+    const int ku = K / 2;
+    const PfScales sc{rows, sa, sb};
+    if (gated) {
+        const dim3 g((N + DC_ROWS - 1) / DC_ROWS, E);
+        if (ku % (2 * DC_KCH) == 0)
+            ffn_decode_i8_kernel<true, 2, 1, true, 1, true, 2><<<g, DC_WAVES * kWave, 0, s>>>(
+                n_rows, N, ku, a, rowmap, topk, offsets, w0, w1, out, sc);
+        else
+            ffn_decode_i8_kernel<true, 1, 1, false, 1, true, 2><<<g, DC_WAVES * kWave, 0, s>>>(
+                n_rows, N, ku, a, rowmap, topk, offsets, w0, w1, out, sc);
+    } else {
+        const dim3 g((N + 4 * DC_ROWS - 1) / (4 * DC_ROWS), E);
+        if (ku % (2 * DC_KCH) == 0)
+            ffn_decode_i8_kernel<false, 2, 2, true, 4, false, 1><<<g, DC_WAVES * kWave, 0, s>>>(
+                n_rows, N, ku, a, rowmap, topk, offsets, w0, w1, out, sc);
+        else
+            ffn_decode_i8_kernel<false, 1, 1, false, 4, false, 1><<<g, DC_WAVES * kWave, 0, s>>>(
+                n_rows, N, ku, a, rowmap, topk, offsets, w0, w1, out, sc);
+    }
     return hipGetLastError();
 }
 

@@ -150,31 +150,6 @@ constexpr int PF_MAX_CPX = 32;  // compute units per XCD the split buffer is siz
 constexpr int PF_DYN_ROUNDS = 2;
 constexpr int PF_DYN_MIN_ROUNDS = 8;
 
-// What a variant of the tiled kernel takes beyond the layer's forward pass:
-// PfKeep (gate/up GEMM of the training pass): both projections are stored too,
-// rounded to bf16; PfScales (8-bit rows and weights): sums of int8 products in
-// int32, scaled by the row's and the weight row's factor in the epilogue.
-struct PfKeep {
-    bf16 *gate, *up;
-};
-struct PfScales {
-    const float *rows, *wa, *wb;
-};
-template <typename... X>
-constexpr bool pf_keeps = (std::is_same<X, PfKeep>::value || ...);
-template <typename... X>
-constexpr bool pf_int8 = (std::is_same<X, PfScales>::value || ...);
-// The extra argument of type T (T() when the variant has none).
-template <typename T>
-__device__ __forceinline__ T pf_extra() {
-    return T{};
-}
-template <typename T, typename X>
-__device__ __forceinline__ T pf_extra(X x) {
-    if constexpr (std::is_same<T, X>::value) return x;
-    else return T{};
-}
-
 // 8-bit rows are addressed in units of two values (the bf16 of the code
 // below), so a stage's 64 units are 128 values of a 128-byte line and
 // everything up to the MFMAs is the same.
@@ -1393,27 +1368,31 @@ hipError_t launch_ffn_prefill_keep(int n_rows, int E, int d, int F, const bf16* 
                                       w.claim + PF_XCD, s);
 }
 
-// 8-bit experts (d and F at least 128).  xq: the quantised grouped rows, or
-// with a row map the tokens'; quantize_act runs between the two GEMMs.
-hipError_t launch_ffn_prefill_i8(int n_rows, int E, int d, int F, const int8_t* xq, const float* xs,
-                                 const int32_t* rowmap, int topk, const int32_t* offsets, const moe_i8_weights& w8,
-                                 bf16* act, int8_t* aq, float* as, int ldf, bf16* h, void* ws, hipStream_t s) {
+// 8-bit experts: the row tiles, then one GEMM each way (K: values, at least 128).
+int launch_plan_i8(int n_rows, int E, const int32_t* offsets, void* ws, RowPlan* plan, hipError_t* err, hipStream_t s) {
     const PfWs w = pf_ws(n_rows, E, ws);
     const int bm = n_rows >= 128 * E ? 256 : 128;  // as prefill_bm
     ffn_plan_kernel<<<1, 1024, 0, s>>>(E, w.max_mt, bm, 0, offsets, w.mt_count, w.mt_expert, w.mt_row0, w.small_count,
                                        w.small_list, w.claim);
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
+    *err = hipGetLastError();
+    *plan = RowPlan{w.mt_count, w.mt_expert, w.mt_row0};
+    return bm;
+}
+
+// A: quantised rows, whose last 128 bytes overlap the line before as
+// launch_quantize_rows writes them (the grouped rows, or with a row map the tokens').
+hipError_t launch_prefill_i8(bool gated, int n_rows, int E, int N, int K, int bm, const int8_t* A, const float* rows,
+                             const int32_t* rowmap, int topk, const int32_t* offsets, const int8_t* wa,
+                             const float* sa, const int8_t* wb, const float* sb, bf16* out, void* ws, hipStream_t s) {
+    const PfWs w = pf_ws(n_rows, E, ws);
     const auto unit = [](const int8_t* v) { return reinterpret_cast<const bf16*>(v); };  // two values
-    err = launch_prefill_gemm<true>(n_rows, F, d / 2, (F + 127) / 128, w.max_mt, bm, E, unit(xq), rowmap, topk,
-                                    w.mt_count, w.mt_expert, w.mt_row0, offsets, unit(w8.w1), unit(w8.w3), act, nullptr,
-                                    w.claim, s, PfScales{xs, w8.s1, w8.s3});
-    if (err != hipSuccess) return err;
-    if ((err = launch_quantize_rows(n_rows, F, ldf, true, MOE_DTYPE_BF16, act, aq, as, offsets + E, s)) != hipSuccess)
-        return err;
-    return launch_prefill_gemm<false>(n_rows, d, F / 2, (d + PF_BN - 1) / PF_BN, w.max_mt, bm, E, unit(aq), nullptr, 1,
-                                      w.mt_count, w.mt_expert, w.mt_row0, offsets, unit(w8.w2), nullptr, h, w.part,
-                                      w.claim + PF_XCD, s, PfScales{as, w8.s2, nullptr});
+    if (gated)
+        return launch_prefill_gemm<true>(n_rows, N, K / 2, (N + 127) / 128, w.max_mt, bm, E, unit(A), rowmap, topk,
+                                         w.mt_count, w.mt_expert, w.mt_row0, offsets, unit(wa), unit(wb), out, nullptr,
+                                         w.claim, s, PfScales{rows, sa, sb});
+    return launch_prefill_gemm<false>(n_rows, N, K / 2, (N + PF_BN - 1) / PF_BN, w.max_mt, bm, E, unit(A), rowmap, topk,
+                                      w.mt_count, w.mt_expert, w.mt_row0, offsets, unit(wa), nullptr, out, w.part,
+                                      w.claim + PF_XCD, s, PfScales{rows, sa, nullptr});
 }
 
 // A plain linear layer (one group of n_rows rows) on the second GEMM's

@@ -3,6 +3,8 @@
 // rows, and explicit wait counts.
 #pragma once
 
+#include <type_traits>
+
 #include "../device_common.h"
 
 namespace moe {
@@ -86,6 +88,32 @@ int prefill_max_mtiles(int n_rows, int E);
 struct RowPlan {
     const int32_t *mt_count = nullptr, *mt_expert = nullptr, *mt_row0 = nullptr;
 };
+// What a variant of the expert-GEMM kernels takes beyond the layer's forward
+// pass:
+// PfKeep (gate/up GEMM of the training pass): both projections are stored too,
+// rounded to bf16; PfScales (8-bit rows and weights): sums of int8 products in
+// int32, scaled by the row's and the weight row's factor in the epilogue.
+struct PfKeep {
+    bf16 *gate, *up;
+};
+struct PfScales {
+    const float *rows, *wa, *wb;
+};
+template <typename... X>
+constexpr bool pf_keeps = (std::is_same<X, PfKeep>::value || ...);
+template <typename... X>
+constexpr bool pf_int8 = (std::is_same<X, PfScales>::value || ...);
+// The extra argument of type T (T() when the variant has none).
+template <typename T>
+__device__ __forceinline__ T pf_extra() {
+    return T{};
+}
+template <typename T, typename X>
+__device__ __forceinline__ T pf_extra(X x) {
+    if constexpr (std::is_same<T, X>::value) return x;
+    else return T{};
+}
+
 // Most row tiles there can be (the plan's grid bound).
 inline int row_plan_tiles(int n_rows, int E, int bm) { return n_rows / bm + E + 1; }
 size_t row_plan_bytes(int n_rows, int E);

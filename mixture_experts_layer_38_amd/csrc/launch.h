@@ -149,10 +149,10 @@ hipError_t launch_route_backward(int T, int d, int E, int K, int dtype, int flag
 // memory; NULL: none) are left alone.
 hipError_t launch_quantize_rows(int64_t rows, int cols, int ldq, bool overlap, int dtype, const void* x, int8_t* q,
                                 float* scale, const int32_t* live, hipStream_t s);
-// n_x rows of x: the n grouped rows (rowmap NULL), or the tokens that grouped
-// row r reads as rowmap[r] / K.
-size_t ffn_i8_ws_bytes(int n_x, int n_rows, int E, int d, int F);
-hipError_t launch_ffn_i8(int n_x, int n_rows, int K, int E, int d, int F, const void* x, const int32_t* rowmap,
+// x: the T * K grouped rows (rowmap NULL), or the T tokens, of which grouped
+// row r reads rowmap[r] / K.
+size_t ffn_i8_ws_bytes(int T, int K, int E, int d, int F, bool by_token);
+hipError_t launch_ffn_i8(int T, int K, int E, int d, int F, const void* x, const int32_t* rowmap,
                          const int32_t* offsets, const moe_i8_weights& w, void* act, void* h, void* ws, hipStream_t s);
 
 }  // namespace moe

@@ -195,7 +195,7 @@ static moe_status forward_launch(const moe_problem* p, const ForwardLayout& L, c
         }
     }
     if (i8)
-        err = launch_ffn_i8(p->T, p->T * p->top_k, p->top_k, p->n_experts, p->d_model, p->d_ff, x, row_assign,
+        err = launch_ffn_i8(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, x, row_assign,
                             offsets, *i8, act, h, i8_ws, s);
     else
         err = launch_ffn(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, p->dtype, x, row_assign,
@@ -224,7 +224,7 @@ static moe_status check_i8(const moe_problem* p, const moe_i8_weights* w) {
 // moe_forward's layout (its act, h and routing scratch), then the 8-bit FFN's workspace.
 static size_t forward_i8_ffn_offset(const moe_problem* p) { return align_up(forward_layout(p).total, 256); }
 static size_t forward_i8_ws_bytes(const moe_problem* p) {
-    return forward_i8_ffn_offset(p) + ffn_i8_ws_bytes(p->T, p->T * p->top_k, p->n_experts, p->d_model, p->d_ff);
+    return forward_i8_ffn_offset(p) + ffn_i8_ws_bytes(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, true);
 }
 
 // ---- allocation-free forward ------------------------------------------------------
@@ -707,8 +707,7 @@ moe_status moe_expert_ffn_i8_workspace_size(const moe_problem* p, size_t* bytes)
     moe_status st = check_i8(p, nullptr);
     if (st != MOE_OK) return st;
     if (!bytes) return MOE_ERR_INVALID_ARG;
-    const int n = p->T * p->top_k;
-    *bytes = ffn_i8_ws_bytes(n, n, p->n_experts, p->d_model, p->d_ff);
+    *bytes = ffn_i8_ws_bytes(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, false);
     return MOE_OK;
 }
 
@@ -722,10 +721,9 @@ moe_status moe_expert_ffn_i8(const moe_problem* p, const void* x_perm, const int
     REQUIRE(offsets);
     REQUIRE(act);
     REQUIRE(h);
-    const int n = p->T * p->top_k;
-    if (!ws || ws_bytes < ffn_i8_ws_bytes(n, n, p->n_experts, p->d_model, p->d_ff)) return MOE_ERR_WORKSPACE;
+    if (!ws || ws_bytes < ffn_i8_ws_bytes(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, false)) return MOE_ERR_WORKSPACE;
     if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
-    return hip_status(launch_ffn_i8(n, n, p->top_k, p->n_experts, p->d_model, p->d_ff, x_perm, nullptr, offsets, *w,
+    return hip_status(launch_ffn_i8(p->T, p->top_k, p->n_experts, p->d_model, p->d_ff, x_perm, nullptr, offsets, *w,
                                     act, h, ws, (hipStream_t)stream));
 }
 
