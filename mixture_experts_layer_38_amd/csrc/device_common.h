@@ -72,6 +72,17 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// Transposing LDS read of a 32 x 16 MFMA operand whose rows lie across k: in each
+// group of 16 lanes, lane 4 r + c addresses four consecutive elements (4 c ..) of
+// k row r at p0, and four k rows on at p1; lane i gets element i of the eight rows.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ bf16x8 read_tr(const bf16* p0, const bf16* p1) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p0);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p1);
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // 8-bit integers with int32 sums: 16 values per lane and operand, in the
 // 16 bytes that hold eight bf16.
 __device__ __forceinline__ i32x16 mfma32_i8(bf16x8 a, bf16x8 b, i32x16 c) {

@@ -52,15 +52,6 @@ struct GradArgs {
     const int32_t* offsets;
 };
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-__device__ __forceinline__ bf16x8 read_tr(const bf16* p0, const bf16* p1) {
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p0);
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p1);
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
 // KT: K is not a multiple of the stage, so a row's chunks past it are masked
 // (rows of the next one otherwise; GRAD_W has no such rows).
 template <int MODE, int BM, bool KT>

@@ -8,6 +8,7 @@
 // Then dx[t] = sum_k dx_perm[row(t,k)] + sum_e dl[t,e] W_r[:,e] and
 // dW_r = x^T dl.  dl stays fp32 throughout.
 #include <algorithm>
+#include <type_traits>
 
 #include "../device_common.h"
 #include "../launch.h"
@@ -100,21 +101,10 @@ __global__ __launch_bounds__(256) void route_dlogits_kernel(int T, int E, int K,
     }
 }
 
-// dx row: the product's sum plus the gradients of the token's grouped rows, slot by slot.
-template <typename T>
-struct EpiTokenGrad {
-    const T* rows;  // may be NULL
-    const int32_t* assign_row;
-    int K, n;
-    T* out;
-    __device__ void operator()(int, int, int m, int c, int N, const f32x4 (&v)[2]) const {
-        f32x4 sum = v[0];
-        if (rows != nullptr)
-            for (int k = 0; k < K; ++k) {
-                const int r = assign_row[(size_t)m * K + k];
-                if ((unsigned)r < (unsigned)n) sum += load_f32x4(rows + (size_t)r * N + c);
-            }
-        store_f32x4(out + (size_t)m * N + c, sum);
+struct EpiProduct {  // fp32 rows of the product
+    float* out;
+    __device__ void operator()(int, int, int m, int n, int N, const f32x4 (&v)[2]) const {
+        store_f32x4(out + (size_t)m * N + n, v[0]);
     }
 };
 struct EpiPart {  // fp32 partial sums [part][M][N]
@@ -139,6 +129,259 @@ __global__ __launch_bounds__(256) void route_dw_reduce_kernel(size_t n, int part
     }
 }
 
+// Eight columns (from c on) of the sum of a token's grouped rows, slot by slot, added to v.
+template <typename T>
+__device__ __forceinline__ void add_rows(float (&v)[8], const T* rows, const int32_t* slots, int K, int n, int d, int c) {
+    constexpr int KC = 8;  // rows whose loads go out together
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int k0 = 0; k0 < K; k0 += KC) {
+        int r[KC];
+        T x[KC][8];
+#pragma unroll
+        for (int k = 0; k < KC; ++k) r[k] = k0 + k < K ? slots[k0 + k] : -1;
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+            if ((unsigned)r[k] < (unsigned)n) __builtin_memcpy(x[k], rows + (size_t)r[k] * d + c, sizeof x[k]);
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+            if ((unsigned)r[k] < (unsigned)n)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += to_f32(x[k][j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += sum[j];
+}
+
+// fp32 layer: adds the grouped rows to the product in dx.
+__global__ __launch_bounds__(256) void route_add_rows_kernel(int T, int K, int d, const float* __restrict__ rows,
+                                                            const int32_t* __restrict__ assign_row,
+                                                            float* __restrict__ dx) {
+    const size_t per = d / 8, total = (size_t)T * per;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
+        const int t = (int)(i / per), c = (int)(i - (size_t)t * per) * 8;
+        float* o = dx + (size_t)t * d + c;
+        float v[8];
+        __builtin_memcpy(v, o, sizeof v);
+        add_rows(v, rows, assign_row + (size_t)t * K, K, T * K, d, c);
+        __builtin_memcpy(o, v, sizeof v);
+    }
+}
+
+// ---- bf16: products on the bf16 MFMAs ------------------------------------------
+// An fp32 score gradient enters as two bf16 values, hi = bf16(v) and lo =
+// bf16(v - hi), so the product with exact bf16 factors is off by at most 2^-18
+// of its terms, below what the sums' fp32 additions lose.
+__device__ __forceinline__ void split8(const float (&v)[8], bf16x8& hi, bf16x8& lo) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        hi[j] = (bf16)v[j];
+        lo[j] = (bf16)(v[j] - (float)hi[j]);
+    }
+}
+// Elements [e, e + 8) of a row of E: one vector each where E is a multiple of 8.
+template <bool VEC>
+__device__ __forceinline__ void load_scores(float (&v)[8], const float* row, int e, int E, bool on) {
+    gm_load8<float, VEC>(v, row + e, on ? E - e : 0);
+}
+template <bool VEC>
+__device__ __forceinline__ bf16x8 load_weights(const bf16* row, int e, int E) {
+    bf16x8 r;
+    if (VEC) {
+        const u32x4 z = {0, 0, 0, 0};
+        r = as_bf16x8(e < E ? load16(row + e) : z);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = e + j < E ? row[e + j] : (bf16)0.0f;
+    }
+    return r;
+}
+
+// dx: a workgroup owns 64 tokens x 256 columns.  The score gradients pass
+// through the LDS (64 experts at a time, split), the router weights come
+// straight from cache; the products then lie in the LDS as fp32 rows (chunks
+// swizzled by row), to which each wave adds the tokens' grouped rows, whole
+// lines at a time.  Bound by those rows (T K d elements).
+constexpr int RX_T = 64, RX_C = 256, RX_E = 64, RX_LD = RX_E + 8;
+template <bool VEC>
+__global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int K, const float* __restrict__ dl,
+                                                      const bf16* __restrict__ wr, const bf16* __restrict__ rows,
+                                                      const int32_t* __restrict__ assign_row, bf16* __restrict__ dx) {
+    __shared__ __align__(16) float sP[RX_T * RX_C];
+    bf16* const sH = reinterpret_cast<bf16*>(sP);  // before sP is filled
+    bf16* const sL = sH + RX_T * RX_LD;
+    const int t0 = blockIdx.x * RX_T, c0 = blockIdx.y * RX_C;
+    const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+    const int fr = lane & 31, fk = (lane >> 5) * 8;
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
+    const int lr = tid >> 2, lc = (tid & 3) * 16;  // row and first column of this thread's part of a chunk
+    for (int e0 = 0; e0 < E; e0 += RX_E) {
+        bf16x8 w[4][2];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb)
+                w[ks][cb] = load_weights<VEC>(wr + (size_t)min(c0 + wave * 64 + cb * 32 + fr, d - 1) * E,
+                                              e0 + ks * 16 + fk, E);
+        const bool on = t0 + lr < T;
+        const float* row = dl + (size_t)min(t0 + lr, T - 1) * E;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            bf16x8 hi, lo;
+            load_scores<VEC>(v, row, e0 + lc + 8 * h, E, on);
+            split8(v, hi, lo);
+            *reinterpret_cast<bf16x8*>(sH + lr * RX_LD + lc + 8 * h) = hi;
+            *reinterpret_cast<bf16x8*>(sL + lr * RX_LD + lc + 8 * h) = lo;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+            if (e0 + ks * 16 < E)
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+                    const bf16x8 hi = *reinterpret_cast<const bf16x8*>(sH + (tb * 32 + fr) * RX_LD + ks * 16 + fk);
+                    const bf16x8 lo = *reinterpret_cast<const bf16x8*>(sL + (tb * 32 + fr) * RX_LD + ks * 16 + fk);
+#pragma unroll
+                    for (int cb = 0; cb < 2; ++cb) {
+                        acc[cb][tb] = mfma32(w[ks][cb], hi, acc[cb][tb]);
+                        acc[cb][tb] = mfma32(w[ks][cb], lo, acc[cb][tb]);
+                    }
+                }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int ch = wave * 16 + cb * 8 + 2 * q + (lane >> 5), t = tb * 32 + fr;
+                const f32x16& a = acc[cb][tb];
+                *reinterpret_cast<f32x4*>(sP + t * RX_C + ((ch ^ (t & 31)) << 2)) =
+                    f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+            }
+    __syncthreads();
+    const int ch = 2 * (lane & 31), c = c0 + (lane & 31) * 8;
+    if (c >= d) return;
+    for (int i = 0; i < RX_T / 8; ++i) {
+        const int tl = wave * (RX_T / 4) + 2 * i + (lane >> 5), t = t0 + tl;
+        if (t >= T) break;
+        const f32x4 a = *reinterpret_cast<const f32x4*>(sP + tl * RX_C + ((ch ^ (tl & 31)) << 2));
+        const f32x4 b = *reinterpret_cast<const f32x4*>(sP + tl * RX_C + (((ch + 1) ^ (tl & 31)) << 2));
+        float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        if (rows != nullptr) add_rows(v, rows, assign_row + (size_t)t * K, K, T * K, d, c);
+        bf16x8 o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = (bf16)v[j];
+        *reinterpret_cast<bf16x8*>(dx + (size_t)t * d + c) = o;
+    }
+}
+
+// dW_r: a workgroup owns 128 columns of x x 128 experts over one part of the
+// tokens, 32 tokens a step.  Both operands lie across the reduction: LDS rows
+// [token][column] with the chunk swizzle and transposing reads of the FFN's
+// weight gradients; the score gradients are split on the way in.
+constexpr int RW_T = 128, RW_K = 32;
+template <bool VEC>
+__global__ __launch_bounds__(256) void route_dw_kernel(int T, int d, int E, const bf16* __restrict__ x,
+                                                      const float* __restrict__ dl, float* __restrict__ part) {
+    __shared__ __align__(16) bf16 sX[2][RW_K * RW_T], sH[2][RW_K * RW_T], sL[2][RW_K * RW_T];
+    const int e0 = blockIdx.x * RW_T, c0 = blockIdx.y * RW_T;
+    const int t_beg = (int)((long long)T * blockIdx.z / gridDim.z);
+    const int t_end = (int)((long long)T * (blockIdx.z + 1) / gridDim.z);
+    const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+    u32x4 rx[2];
+    float rd[2][8];
+    const int lr = tid >> 4, lch = tid & 15;  // token (and the one 16 on) and chunk of this thread
+    auto load = [&](int t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = t + lr + 16 * h;
+            const bool on = r < t_end;
+            rx[h] = load16_or_zero(x + (size_t)r * d + c0 + lch * 8, on && c0 + lch * 8 < d);
+            load_scores<VEC>(rd[h], dl + (size_t)r * E, e0 + lch * 8, E, on);
+        }
+    };
+    auto store = [&](int buf) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = (lr + 16 * h) * RW_T + ((lch ^ ((lr & 3) << 2)) << 3);
+            bf16x8 hi, lo;
+            split8(rd[h], hi, lo);
+            store16(&sX[buf][at], rx[h]);
+            *reinterpret_cast<bf16x8*>(&sH[buf][at]) = hi;
+            *reinterpret_cast<bf16x8*>(&sL[buf][at]) = lo;
+        }
+    };
+    const int wm = wave & 1, wn = wave >> 1;
+    const int fhalf = lane >> 5, g16 = (lane >> 4) & 1, rr = (lane >> 2) & 3, cc = lane & 3;
+    int off[2][2];  // [x or scores][block]
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int in = 2 * g16 + (cc >> 1);
+        off[0][b] = (8 * fhalf + rr) * RW_T + (((8 * wm + 4 * b + in) ^ (rr << 2)) << 3) + (cc & 1) * 4;
+        off[1][b] = (8 * fhalf + rr) * RW_T + (((8 * wn + 4 * b + in) ^ (rr << 2)) << 3) + (cc & 1) * 4;
+    }
+    auto frag = [&](const bf16* s, int o, int q) {
+        return read_tr(s + o + 16 * q * RW_T, s + o + (16 * q + 4) * RW_T);
+    };
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
+    load(t_beg);
+    store(0);
+    __syncthreads();
+    int buf = 0;
+    for (int t = t_beg; t < t_end; t += RW_K, buf ^= 1) {
+        const bool more = t + RW_K < t_end;
+        if (more) load(t + RW_K);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            bf16x8 m[2], hi[2], lo[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                m[b] = frag(sX[buf], off[0][b], q);
+                hi[b] = frag(sH[buf], off[1][b], q);
+                lo[b] = frag(sL[buf], off[1][b], q);
+            }
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int mb = 0; mb < 2; ++mb) {
+                    acc[nb][mb] = mfma32(hi[nb], m[mb], acc[nb][mb]);
+                    acc[nb][mb] = mfma32(lo[nb], m[mb], acc[nb][mb]);
+                }
+        }
+        if (more) store(buf ^ 1);
+        __syncthreads();
+    }
+    const EpiPart epi{part, d};
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb) {
+        const int c = c0 + wm * 64 + mb * 32 + (lane & 31);
+        if (c >= d) continue;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int e = e0 + wn * 64 + nb * 32 + 8 * q + 4 * fhalf;
+                const f32x16& a = acc[nb][mb];
+                const f32x4 v[2] = {f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]}, f32x4{}};
+                if (e < E) epi(blockIdx.z, 0, c, e, E, v);
+            }
+    }
+}
+
 // Parts of the sum over the tokens: enough workgroups for two per compute
 // unit, at least 128 tokens each.
 int dw_parts(int T, int d, int E) {
@@ -146,29 +389,63 @@ int dw_parts(int T, int d, int E) {
     return std::max(1, std::min((512 + tiles - 1) / tiles, (T + 127) / 128));
 }
 
-template <typename T, bool VEC>
-hipError_t route_products(int n_tok, int d, int E, int K, const T* x, const T* wr, const T* dx_perm,
-                          const int32_t* assign_row, const float* dl, T* dx, T* dwr, float* part, hipStream_t s) {
+template <bool VEC>
+hipError_t route_products(int n_tok, int d, int E, int K, const float* x, const float* wr, const float* dx_perm,
+                          const int32_t* assign_row, const float* dl, float* dx, float* dwr, float* part, int parts,
+                          hipStream_t s) {
     const unsigned td = (d + GM_T - 1) / GM_T;
     hipError_t err;
     if (dx != nullptr) {
-        GemmArgs<float, T> g{{dl, nullptr}, {wr, nullptr}, E, E, 0, 0, d, E, n_tok, 1, RowPlan{}, nullptr};
-        gemm_f32_kernel<GM_NT, false, 1, VEC, VEC><<<dim3((n_tok + GM_T - 1) / GM_T, td), 256, 0, s>>>(
-            g, EpiTokenGrad<T>{dx_perm, assign_row, K, n_tok * K, dx});
+        GemmArgs<float, float> g{{dl, nullptr}, {wr, nullptr}, E, E, 0, 0, d, E, n_tok, 1, RowPlan{}, nullptr};
+        gemm_f32_kernel<GM_NT, false, 1, VEC, VEC><<<dim3((n_tok + GM_T - 1) / GM_T, td), 256, 0, s>>>(g, EpiProduct{dx});
         if ((err = hipGetLastError()) != hipSuccess) return err;
+        if (dx_perm != nullptr) {
+            const size_t vecs = (size_t)n_tok * d / 8;
+            route_add_rows_kernel<<<(unsigned)std::min<size_t>((vecs + 255) / 256, 1 << 20), 256, 0, s>>>(
+                n_tok, K, d, dx_perm, assign_row, dx);
+            if ((err = hipGetLastError()) != hipSuccess) return err;
+        }
     }
     if (dwr != nullptr) {
-        const int parts = dw_parts(n_tok, d, E);
-        GemmArgs<T, float> g{{x, nullptr}, {dl, nullptr}, d, E, 0, d, E, 0, n_tok, 1, RowPlan{}, nullptr};
+        GemmArgs<float, float> g{{x, nullptr}, {dl, nullptr}, d, E, 0, d, E, 0, n_tok, 1, RowPlan{}, nullptr};
         gemm_f32_kernel<GM_TN, false, 1, true, VEC><<<dim3((E + GM_T - 1) / GM_T, td, parts), 256, 0, s>>>(
             g, EpiPart{part, d});
         if ((err = hipGetLastError()) != hipSuccess) return err;
-        const size_t n = (size_t)d * E;
-        route_dw_reduce_kernel<T><<<(unsigned)std::min<size_t>((n + 255) / 256, 4096), 256, 0, s>>>(n, parts, part,
-                                                                                                   dwr);
+    }
+    return hipSuccess;
+}
+
+template <bool VEC>
+hipError_t route_products(int n_tok, int d, int E, int K, const bf16* x, const bf16* wr, const bf16* dx_perm,
+                          const int32_t* assign_row, const float* dl, bf16* dx, bf16* dwr, float* part, int parts,
+                          hipStream_t s) {
+    hipError_t err;
+    if (dx != nullptr) {
+        route_dx_kernel<VEC><<<dim3((n_tok + RX_T - 1) / RX_T, (d + RX_C - 1) / RX_C), 256, 0, s>>>(
+            n_tok, d, E, K, dl, wr, dx_perm, assign_row, dx);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
+    if (dwr != nullptr) {
+        route_dw_kernel<VEC><<<dim3((E + RW_T - 1) / RW_T, (d + RW_T - 1) / RW_T, parts), 256, 0, s>>>(n_tok, d, E, x, dl,
+                                                                                                       part);
         if ((err = hipGetLastError()) != hipSuccess) return err;
     }
     return hipSuccess;
+}
+
+template <typename T>
+hipError_t route_gradients(int n_tok, int d, int E, int K, const void* x, const void* wr, const void* dx_perm,
+                           const int32_t* assign_row, const float* dl, void* dx, void* dwr, float* part, hipStream_t s) {
+    const int parts = dw_parts(n_tok, d, E);
+    const auto run = [&](auto vec) {  // rows of E elements in whole vectors or not
+        return route_products<decltype(vec)::value>(n_tok, d, E, K, (const T*)x, (const T*)wr, (const T*)dx_perm,
+                                                    assign_row, dl, (T*)dx, (T*)dwr, part, parts, s);
+    };
+    const hipError_t err = E % 8 == 0 ? run(std::true_type{}) : run(std::false_type{});
+    if (err != hipSuccess || dwr == nullptr) return err;
+    const size_t n = (size_t)d * E;
+    route_dw_reduce_kernel<T><<<(unsigned)std::min<size_t>((n + 255) / 256, 4096), 256, 0, s>>>(n, parts, part, (T*)dwr);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -192,17 +469,9 @@ hipError_t launch_route_backward(int T, int d, int E, int K, int dtype, int flag
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     float* part = (float*)ws;
-    const bool vec = E % 8 == 0;
-    if (dtype == MOE_DTYPE_F32)
-        err = vec ? route_products<float, true>(T, d, E, K, (const float*)x, (const float*)wr, (const float*)dx_perm,
-                                                assign_row, dl, (float*)dx, (float*)dwr, part, s)
-                  : route_products<float, false>(T, d, E, K, (const float*)x, (const float*)wr, (const float*)dx_perm,
-                                                 assign_row, dl, (float*)dx, (float*)dwr, part, s);
-    else
-        err = vec ? route_products<bf16, true>(T, d, E, K, (const bf16*)x, (const bf16*)wr, (const bf16*)dx_perm,
-                                               assign_row, dl, (bf16*)dx, (bf16*)dwr, part, s)
-                  : route_products<bf16, false>(T, d, E, K, (const bf16*)x, (const bf16*)wr, (const bf16*)dx_perm,
-                                                assign_row, dl, (bf16*)dx, (bf16*)dwr, part, s);
+    err = dtype == MOE_DTYPE_F32
+              ? route_gradients<float>(T, d, E, K, x, wr, dx_perm, assign_row, dl, dx, dwr, part, s)
+              : route_gradients<bf16>(T, d, E, K, x, wr, dx_perm, assign_row, dl, dx, dwr, part, s);
     if (err == hipSuccess) timer_after(MOE_KERNEL_ROUTE_BACKWARD, s);
     return err;
 }
