@@ -118,14 +118,14 @@ struct EpiPart {  // fp32 partial sums [part][M][N]
     }
 };
 
-// Adds the parts in order.
+// Adds the parts in order (n is a multiple of 8).
 template <typename T>
 __global__ __launch_bounds__(256) void route_dw_reduce_kernel(size_t n, int parts, const float* __restrict__ part,
                                                              T* __restrict__ out) {
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
-        float v = part[i];
-        for (int p = 1; p < parts; ++p) v += part[(size_t)p * n + i];
-        out[i] = from_f32<T>(v);
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (size_t)gridDim.x * 1024) {
+        f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
+        for (int p = 1; p < parts; ++p) v += *reinterpret_cast<const f32x4*>(part + (size_t)p * n + i);
+        store_f32x4(out + i, v);
     }
 }
 
@@ -196,12 +196,12 @@ __device__ __forceinline__ bf16x8 load_weights(const bf16* row, int e, int E) {
     return r;
 }
 
-// dx: a workgroup owns 64 tokens x 256 columns.  The score gradients pass
+// dx: a workgroup owns 64 tokens x 128 columns.  The score gradients pass
 // through the LDS (64 experts at a time, split), the router weights come
 // straight from cache; the products then lie in the LDS as fp32 rows (chunks
 // swizzled by row), to which each wave adds the tokens' grouped rows, whole
 // lines at a time.  Bound by those rows (T K d elements).
-constexpr int RX_T = 64, RX_C = 256, RX_E = 64, RX_LD = RX_E + 8;
+constexpr int RX_T = 64, RX_C = 128, RX_E = 64, RX_LD = RX_E + 8;
 template <bool VEC>
 __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int K, const float* __restrict__ dl,
                                                       const bf16* __restrict__ wr, const bf16* __restrict__ rows,
@@ -212,34 +212,37 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
     const int t0 = blockIdx.x * RX_T, c0 = blockIdx.y * RX_C;
     const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
     const int fr = lane & 31, fk = (lane >> 5) * 8;
-    f32x16 acc[2][2];
+    f32x16 acc[2];
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) acc[b][i] = 0.0f;
     const int lr = tid >> 2, lc = (tid & 3) * 16;  // row and first column of this thread's part of a chunk
+    const bf16* wrow = wr + (size_t)min(c0 + wave * 32 + fr, d - 1) * E;
+    const bool on = t0 + lr < T;
+    const float* drow = dl + (size_t)min(t0 + lr, T - 1) * E;
+    bf16x8 w[4];
+    float v[2][8];
+    auto load = [&](int e0) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) w[ks] = load_weights<VEC>(wrow, e0 + ks * 16 + fk, E);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) load_scores<VEC>(v[h], drow, e0 + lc + 8 * h, E, on);
+    };
+    load(0);
     for (int e0 = 0; e0 < E; e0 += RX_E) {
-        bf16x8 w[4][2];
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-            for (int cb = 0; cb < 2; ++cb)
-                w[ks][cb] = load_weights<VEC>(wr + (size_t)min(c0 + wave * 64 + cb * 32 + fr, d - 1) * E,
-                                              e0 + ks * 16 + fk, E);
-        const bool on = t0 + lr < T;
-        const float* row = dl + (size_t)min(t0 + lr, T - 1) * E;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float v[8];
             bf16x8 hi, lo;
-            load_scores<VEC>(v, row, e0 + lc + 8 * h, E, on);
-            split8(v, hi, lo);
+            split8(v[h], hi, lo);
             *reinterpret_cast<bf16x8*>(sH + lr * RX_LD + lc + 8 * h) = hi;
             *reinterpret_cast<bf16x8*>(sL + lr * RX_LD + lc + 8 * h) = lo;
         }
+        bf16x8 cw[4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) cw[ks] = w[ks];
         __syncthreads();
+        if (e0 + RX_E < E) load(e0 + RX_E);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
             if (e0 + ks * 16 < E)
@@ -247,76 +250,72 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
                 for (int tb = 0; tb < 2; ++tb) {
                     const bf16x8 hi = *reinterpret_cast<const bf16x8*>(sH + (tb * 32 + fr) * RX_LD + ks * 16 + fk);
                     const bf16x8 lo = *reinterpret_cast<const bf16x8*>(sL + (tb * 32 + fr) * RX_LD + ks * 16 + fk);
-#pragma unroll
-                    for (int cb = 0; cb < 2; ++cb) {
-                        acc[cb][tb] = mfma32(w[ks][cb], hi, acc[cb][tb]);
-                        acc[cb][tb] = mfma32(w[ks][cb], lo, acc[cb][tb]);
-                    }
+                    acc[tb] = mfma32(cw[ks], hi, acc[tb]);
+                    acc[tb] = mfma32(cw[ks], lo, acc[tb]);
                 }
         __syncthreads();
     }
 #pragma unroll
-    for (int cb = 0; cb < 2; ++cb)
+    for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int ch = wave * 16 + cb * 8 + 2 * q + (lane >> 5), t = tb * 32 + fr;
-                const f32x16& a = acc[cb][tb];
-                *reinterpret_cast<f32x4*>(sP + t * RX_C + ((ch ^ (t & 31)) << 2)) =
-                    f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
-            }
+        for (int q = 0; q < 4; ++q) {
+            const int ch = wave * 8 + 2 * q + (lane >> 5), t = tb * 32 + fr;
+            *reinterpret_cast<f32x4*>(sP + t * RX_C + ((ch ^ (t & 31)) << 2)) =
+                f32x4{acc[tb][4 * q], acc[tb][4 * q + 1], acc[tb][4 * q + 2], acc[tb][4 * q + 3]};
+        }
     __syncthreads();
-    const int ch = 2 * (lane & 31), c = c0 + (lane & 31) * 8;
+    const int ch = 2 * (lane & 15), c = c0 + (lane & 15) * 8;
     if (c >= d) return;
-    for (int i = 0; i < RX_T / 8; ++i) {
-        const int tl = wave * (RX_T / 4) + 2 * i + (lane >> 5), t = t0 + tl;
+#pragma unroll 2
+    for (int i = 0; i < RX_T / 16; ++i) {
+        const int tl = wave * (RX_T / 4) + 4 * i + (lane >> 4), t = t0 + tl;
         if (t >= T) break;
         const f32x4 a = *reinterpret_cast<const f32x4*>(sP + tl * RX_C + ((ch ^ (tl & 31)) << 2));
         const f32x4 b = *reinterpret_cast<const f32x4*>(sP + tl * RX_C + (((ch + 1) ^ (tl & 31)) << 2));
-        float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        if (rows != nullptr) add_rows(v, rows, assign_row + (size_t)t * K, K, T * K, d, c);
+        float sum[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        if (rows != nullptr) add_rows(sum, rows, assign_row + (size_t)t * K, K, T * K, d, c);
         bf16x8 o;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = (bf16)v[j];
+        for (int j = 0; j < 8; ++j) o[j] = (bf16)sum[j];
         *reinterpret_cast<bf16x8*>(dx + (size_t)t * d + c) = o;
     }
 }
 
 // dW_r: a workgroup owns 128 columns of x x 128 experts over one part of the
-// tokens, 32 tokens a step.  Both operands lie across the reduction: LDS rows
+// tokens, 64 tokens a step (the next step's loads in flight meanwhile: with 32
+// each step waited for them, 74 us).  Both operands lie across the reduction: LDS rows
 // [token][column] with the chunk swizzle and transposing reads of the FFN's
 // weight gradients; the score gradients are split on the way in.
-constexpr int RW_T = 128, RW_K = 32;
+constexpr int RW_T = 128, RW_K = 64, RW_H = RW_K / 16;
 template <bool VEC>
 __global__ __launch_bounds__(256) void route_dw_kernel(int T, int d, int E, const bf16* __restrict__ x,
                                                       const float* __restrict__ dl, float* __restrict__ part) {
-    __shared__ __align__(16) bf16 sX[2][RW_K * RW_T], sH[2][RW_K * RW_T], sL[2][RW_K * RW_T];
+    __shared__ __align__(16) bf16 sX[RW_K * RW_T], sH[RW_K * RW_T], sL[RW_K * RW_T];
     const int e0 = blockIdx.x * RW_T, c0 = blockIdx.y * RW_T;
     const int t_beg = (int)((long long)T * blockIdx.z / gridDim.z);
     const int t_end = (int)((long long)T * (blockIdx.z + 1) / gridDim.z);
     const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
-    u32x4 rx[2];
-    float rd[2][8];
-    const int lr = tid >> 4, lch = tid & 15;  // token (and the one 16 on) and chunk of this thread
+    u32x4 rx[RW_H];
+    float rd[RW_H][8];
+    const int lr = tid >> 4, lch = tid & 15;  // token (and those 16, 32, 48 on) and chunk of this thread
     auto load = [&](int t) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < RW_H; ++h) {
             const int r = t + lr + 16 * h;
             const bool on = r < t_end;
             rx[h] = load16_or_zero(x + (size_t)r * d + c0 + lch * 8, on && c0 + lch * 8 < d);
             load_scores<VEC>(rd[h], dl + (size_t)r * E, e0 + lch * 8, E, on);
         }
     };
-    auto store = [&](int buf) {
+    auto store = [&]() {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < RW_H; ++h) {
             const int at = (lr + 16 * h) * RW_T + ((lch ^ ((lr & 3) << 2)) << 3);
             bf16x8 hi, lo;
             split8(rd[h], hi, lo);
-            store16(&sX[buf][at], rx[h]);
-            *reinterpret_cast<bf16x8*>(&sH[buf][at]) = hi;
-            *reinterpret_cast<bf16x8*>(&sL[buf][at]) = lo;
+            store16(&sX[at], rx[h]);
+            *reinterpret_cast<bf16x8*>(&sH[at]) = hi;
+            *reinterpret_cast<bf16x8*>(&sL[at]) = lo;
         }
     };
     const int wm = wave & 1, wn = wave >> 1;
@@ -339,20 +338,18 @@ __global__ __launch_bounds__(256) void route_dw_kernel(int T, int d, int E, cons
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
     load(t_beg);
-    store(0);
-    __syncthreads();
-    int buf = 0;
-    for (int t = t_beg; t < t_end; t += RW_K, buf ^= 1) {
-        const bool more = t + RW_K < t_end;
-        if (more) load(t + RW_K);
+    for (int t = t_beg; t < t_end; t += RW_K) {
+        store();
+        __syncthreads();
+        if (t + RW_K < t_end) load(t + RW_K);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < RW_K / 16; ++q) {
             bf16x8 m[2], hi[2], lo[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                m[b] = frag(sX[buf], off[0][b], q);
-                hi[b] = frag(sH[buf], off[1][b], q);
-                lo[b] = frag(sL[buf], off[1][b], q);
+                m[b] = frag(sX, off[0][b], q);
+                hi[b] = frag(sH, off[1][b], q);
+                lo[b] = frag(sL, off[1][b], q);
             }
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb)
@@ -362,7 +359,6 @@ __global__ __launch_bounds__(256) void route_dw_kernel(int T, int d, int E, cons
                     acc[nb][mb] = mfma32(lo[nb], m[mb], acc[nb][mb]);
                 }
         }
-        if (more) store(buf ^ 1);
         __syncthreads();
     }
     const EpiPart epi{part, d};
@@ -382,11 +378,12 @@ __global__ __launch_bounds__(256) void route_dw_kernel(int T, int d, int E, cons
     }
 }
 
-// Parts of the sum over the tokens: enough workgroups for two per compute
-// unit, at least 128 tokens each.
+// Parts of the sum over the tokens: at most two workgroups per compute unit,
+// which all run at once (five parts instead of four on 112 tiles, 560
+// workgroups: 83 us), at least 128 tokens each.
 int dw_parts(int T, int d, int E) {
     const int tiles = ((d + GM_T - 1) / GM_T) * ((E + GM_T - 1) / GM_T);
-    return std::max(1, std::min((512 + tiles - 1) / tiles, (T + 127) / 128));
+    return std::max(1, std::min(512 / tiles, (T + 127) / 128));
 }
 
 template <bool VEC>
@@ -444,7 +441,7 @@ hipError_t route_gradients(int n_tok, int d, int E, int K, const void* x, const 
     const hipError_t err = E % 8 == 0 ? run(std::true_type{}) : run(std::false_type{});
     if (err != hipSuccess || dwr == nullptr) return err;
     const size_t n = (size_t)d * E;
-    route_dw_reduce_kernel<T><<<(unsigned)std::min<size_t>((n + 255) / 256, 4096), 256, 0, s>>>(n, parts, part, (T*)dwr);
+    route_dw_reduce_kernel<T><<<(unsigned)std::min<size_t>((n + 1023) / 1024, 4096), 256, 0, s>>>(n, parts, part, (T*)dwr);
     return hipGetLastError();
 }
 
