@@ -1168,14 +1168,15 @@ size_t prefill_ws_bytes(int n_rows, int E, int d) {
     return prefill_plan_bytes(n_rows, E) + prefill_split_bytes(n_rows, E, d);
 }
 
-// A plan without the small-expert list: [mt_count][small_count][mt_expert][mt_row0].
+// A plan without the small-expert list: [mt_count][small_count][mt_expert][mt_row0],
+// for tiles of 64 rows or more.
 size_t row_plan_bytes(int n_rows, int E) {
-    return align_up((size_t)(2 + 2 * prefill_max_mtiles(n_rows, E)) * sizeof(int32_t), 256);
+    return align_up((size_t)(2 + 2 * row_plan_tiles(n_rows, E, 64)) * sizeof(int32_t), 256);
 }
 
 hipError_t launch_row_plan(int n_rows, int E, int bm, const int32_t* offsets, void* ws, RowPlan* plan,
                            hipStream_t s) {
-    const int max_mt = prefill_max_mtiles(n_rows, E);
+    const int max_mt = row_plan_tiles(n_rows, E, bm);
     int32_t* w = reinterpret_cast<int32_t*>(ws);
     *plan = RowPlan{w, w + 2, w + 2 + max_mt};
     ffn_plan_kernel<<<1, 1024, 0, s>>>(E, max_mt, bm, 0, offsets, w, w + 2, w + 2 + max_mt, w + 1, nullptr, nullptr);

@@ -5,6 +5,9 @@
 //   dx = W1^T dg + W3^T du;  dW1 = sum dg a^T;  dW3 = sum du a^T;  dW2 = sum dh act^T
 // g and u are stored in the layer type; act is formed again from them in the
 // backward pass (two stored rows of F instead of three).
+#include <algorithm>
+#include <type_traits>
+
 #include "../device_common.h"
 #include "../launch.h"
 #include "ffn_tiles.h"
@@ -75,49 +78,65 @@ struct EpiWeights {  // C is one expert's [M][N]
     }
 };
 
+// Calls f with the tile for this many rows and columns as a compile-time constant.
+template <typename F>
+hipError_t with_tile(int tile, F f) {
+    return tile == 64 ? f(std::integral_constant<int, 64>{}) : f(std::integral_constant<int, 128>{});
+}
+unsigned tiles_of(int v, int tile) { return (unsigned)((v + tile - 1) / tile); }
+int rows_tile(int n, int E, int cols) { return gm_tile((long)row_plan_tiles(n, E, 128) * tiles_of(cols, 128)); }
+
+template <int LAYOUT, bool DUAL, int SEGS, typename Epi>
+hipError_t rows_product(int tile, const GemmArgs<float, float>& g, Epi epi, hipStream_t s) {
+    return with_tile(tile, [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        gemm_f32_kernel<T, LAYOUT, DUAL, SEGS, true, true>
+            <<<dim3((unsigned)row_plan_tiles(g.n_rows, g.E, T), tiles_of(g.N, T)), 256, 0, s>>>(g, epi);
+        return hipGetLastError();
+    });
+}
+hipError_t weight_product(const GemmArgs<float, float>& g, int sels, EpiWeights<float> epi, hipStream_t s) {
+    const int tile = gm_tile((long)tiles_of(g.M, 128) * tiles_of(g.N, 128) * g.E * sels);
+    return with_tile(tile, [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        gemm_f32_kernel<T, GM_TN, false, 1, true, true>
+            <<<dim3(tiles_of(g.N, T), tiles_of(g.M, T), g.E * sels), 256, 0, s>>>(g, epi);
+        return hipGetLastError();
+    });
+}
+
+// tile: the plan's row tiles, which are the products' tiles too.
 hipError_t train_gemms(int n, int E, int d, int F, const float* x, const int32_t* offsets, const float* w1,
-                       const float* w3, const float* w2, float* gate, float* up, float* act, float* h,
+                       const float* w3, const float* w2, float* gate, float* up, float* act, float* h, int tile,
                        const RowPlan& plan, hipStream_t s) {
     typedef float T;
-    const unsigned mt = (unsigned)row_plan_tiles(n, E, GM_T);
     GemmArgs<T, T> g{{x, nullptr}, {w1, w3}, d, d, (size_t)F * d, 0, F, d, n, E, plan, offsets};
-    gemm_f32_kernel<GM_NT, true, 1, true, true><<<dim3(mt, (F + GM_T - 1) / GM_T), 256, 0, s>>>(
-        g, EpiGate<T>{gate, up, act});
-    hipError_t err = hipGetLastError();
+    const hipError_t err = rows_product<GM_NT, true, 1>(tile, g, EpiGate<T>{gate, up, act}, s);
     if (err != hipSuccess) return err;
     GemmArgs<T, T> g2{{act, nullptr}, {w2, nullptr}, F, F, (size_t)F * d, 0, d, F, n, E, plan, offsets};
-    gemm_f32_kernel<GM_NT, false, 1, true, true><<<dim3(mt, (d + GM_T - 1) / GM_T), 256, 0, s>>>(g2, EpiRows<T>{h});
-    return hipGetLastError();
+    return rows_product<GM_NT, false, 1>(tile, g2, EpiRows<T>{h}, s);
 }
 
 hipError_t backward_gemms(int n, int E, int d, int F, const float* x, const int32_t* offsets, const float* w1,
                           const float* w3, const float* w2, const float* gate, const float* up, const float* dh,
                           float* dx, float* dw1, float* dw3, float* dw2, float* dgate, float* dup, float* act,
-                          const RowPlan& plan, hipStream_t s) {
+                          int tile, const RowPlan& plan, hipStream_t s) {
     typedef float T;
-    const unsigned mt = (unsigned)row_plan_tiles(n, E, GM_T);
-    const unsigned td = (d + GM_T - 1) / GM_T, tf = (F + GM_T - 1) / GM_T;
     const size_t ws = (size_t)F * d;
     GemmArgs<T, T> ga{{dh, nullptr}, {w2, nullptr}, d, F, ws, 0, F, d, n, E, plan, offsets};
-    gemm_f32_kernel<GM_NN, false, 1, true, true><<<dim3(mt, tf), 256, 0, s>>>(
-        ga, EpiGateGrad<T>{gate, up, dgate, dup, act});
-    hipError_t err = hipGetLastError();
+    hipError_t err = rows_product<GM_NN, false, 1>(tile, ga, EpiGateGrad<T>{gate, up, dgate, dup, act}, s);
     if (err != hipSuccess) return err;
     if (dw2 != nullptr) {
         GemmArgs<T, T> g{{dh, nullptr}, {act, nullptr}, d, F, 0, d, F, 0, n, E, RowPlan{}, offsets};
-        gemm_f32_kernel<GM_TN, false, 1, true, true><<<dim3(tf, td, E), 256, 0, s>>>(g, EpiWeights<T>{dw2, nullptr, d});
-        if ((err = hipGetLastError()) != hipSuccess) return err;
+        if ((err = weight_product(g, 1, EpiWeights<T>{dw2, nullptr, d}, s)) != hipSuccess) return err;
         GemmArgs<T, T> g13{{dgate, dup}, {x, nullptr}, F, d, 0, F, d, 0, n, E, RowPlan{}, offsets};
-        gemm_f32_kernel<GM_TN, false, 1, true, true><<<dim3(td, tf, 2 * E), 256, 0, s>>>(g13,
-                                                                                        EpiWeights<T>{dw1, dw3, F});
-        if ((err = hipGetLastError()) != hipSuccess) return err;
+        if ((err = weight_product(g13, 2, EpiWeights<T>{dw1, dw3, F}, s)) != hipSuccess) return err;
     }
     if (dx != nullptr) {
         GemmArgs<T, T> g{{dgate, dup}, {w1, w3}, F, d, ws, 0, d, F, n, E, plan, offsets};
-        gemm_f32_kernel<GM_NN, false, 2, true, true><<<dim3(mt, td), 256, 0, s>>>(g, EpiRows<T>{dx});
-        if ((err = hipGetLastError()) != hipSuccess) return err;
+        err = rows_product<GM_NN, false, 2>(tile, g, EpiRows<T>{dx}, s);
     }
-    return hipSuccess;
+    return err;
 }
 
 }  // namespace
@@ -140,9 +159,10 @@ hipError_t launch_ffn_train(int T, int K, int E, int d, int F, int dtype, const 
     timer_before(MOE_KERNEL_FFN_TRAIN, s);
     if (dtype == MOE_DTYPE_F32) {
         RowPlan plan;
-        if ((err = launch_row_plan(n, E, GM_T, offsets, rest, &plan, s)) != hipSuccess) return err;
+        const int tile = rows_tile(n, E, std::min(d, F));
+        if ((err = launch_row_plan(n, E, tile, offsets, rest, &plan, s)) != hipSuccess) return err;
         err = train_gemms(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3, (const float*)w2,
-                          (float*)gate, (float*)up, (float*)base, (float*)h, plan, s);
+                          (float*)gate, (float*)up, (float*)base, (float*)h, tile, plan, s);
     } else {
         err = launch_ffn_prefill_keep(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3,
                                       (const bf16*)w2, (bf16*)gate, (bf16*)up, (bf16*)base, (bf16*)h, rest, s);
@@ -169,10 +189,12 @@ hipError_t launch_ffn_backward(int T, int K, int E, int d, int F, int dtype, con
     timer_before(MOE_KERNEL_FFN_BACKWARD, s);
     if (dtype == MOE_DTYPE_F32) {
         RowPlan plan;
-        if ((err = launch_row_plan(n, E, GM_T, offsets, rest, &plan, s)) != hipSuccess) return err;
+        const int tile = rows_tile(n, E, std::min(d, F));
+        if ((err = launch_row_plan(n, E, tile, offsets, rest, &plan, s)) != hipSuccess) return err;
         err = backward_gemms(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3,
                              (const float*)w2, (const float*)gate, (const float*)up, (const float*)dh, (float*)dx,
-                             (float*)dw1, (float*)dw3, (float*)dw2, (float*)dgate, (float*)dup, (float*)act, plan, s);
+                             (float*)dw1, (float*)dw3, (float*)dw2, (float*)dgate, (float*)dup, (float*)act, tile, plan,
+                             s);
     } else {
         err = launch_ffn_grad(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3, (const bf16*)w2,
                               (const bf16*)gate, (const bf16*)up, (const bf16*)dh, (bf16*)dx, (bf16*)dw1, (bf16*)dw3,

@@ -1,4 +1,4 @@
-// Grouped matrix products in fp32: 128 x 128 output tiles on the fp32 MFMA
+// Grouped matrix products in fp32: square output tiles on the fp32 MFMA
 // (v_mfma_f32_32x32x2_f32, exact products, fp32 sums in a fixed order), for
 // the fp32 layer and for operands that must not be rounded to bf16.  bf16
 // operands are widened on the way into the LDS.
@@ -7,9 +7,12 @@
 //   GM_NN  C[r][n] = sum_k A[r][k] B[k][n]
 //   GM_TN  C[m][n] = sum_r A[r][m] B[r][n]     the sum runs over the group's rows
 //
-// A workgroup of four waves owns a tile; wave (wm, wn) owns 64 x 64 of it.
-// Operands go through registers (the next 16-wide k step is loaded while the
-// present one is multiplied) into LDS tiles [k][row], padded so that the
+// A workgroup of four waves (2 x 2) owns a tile of 128, or of 64 where tiles of
+// 128 would leave compute units idle: the MFMAs of a 128-wide tile take 14 us
+// per 128 of k and product pair, whatever its rows hold (64 rows over 8 experts,
+// d 128, F 256: 21 us a product with tiles of 128).
+// Operands go through registers (the next k step is loaded while the present
+// one is multiplied) into LDS tiles [k][row], padded so that the
 // column reads of the MFMA operands and the transposing writes fall in
 // distinct banks.
 #pragma once
@@ -19,9 +22,9 @@
 
 namespace moe {
 
-constexpr int GM_T = 128;        // tile rows and columns
-constexpr int GM_K = 16;         // k per step
-constexpr int GM_LD = GM_T + 4;  // padded LDS row (floats)
+constexpr int GM_K = 32;  // k per step
+// The tile for a launch of `tiles` tiles of 128.
+inline int gm_tile(long tiles) { return tiles < 512 ? 64 : 128; }
 enum { GM_NT, GM_NN, GM_TN };
 
 // One product of every group.  a[1], b[1]: the second factor pair where the
@@ -72,9 +75,12 @@ __device__ __forceinline__ void gm_load8(float (&r)[8], const T* p, int left) {
 // epi(e, sel, m, n, N, v) for four consecutive columns n .. n + 3 of row m
 // (grouped row, or A's column for GM_TN) with the sums v[0] (and v[1] of the
 // second product).
-template <int LAYOUT, bool DUAL, int SEGS, bool VA, bool VB, typename TA, typename TB, typename Epi>
+template <int GM_T, int LAYOUT, bool DUAL, int SEGS, bool VA, bool VB, typename TA, typename TB, typename Epi>
 __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi epi) {
     constexpr int NB = DUAL ? 2 : 1;
+    constexpr int GM_LD = GM_T + 4;             // padded LDS row (floats)
+    constexpr int GM_H = GM_T * GM_K / 8 / 256;  // 8-element vectors per thread and operand
+    constexpr int BL = GM_T / 64;               // 32 x 32 blocks per wave and side
     __shared__ __align__(16) float sA[GM_K][GM_LD];
     __shared__ __align__(16) float sB[NB][GM_K][GM_LD];
     const int tid = threadIdx.x;
@@ -106,51 +112,63 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi e
         m_end = g.n_rows;
     }
 
-    const int kr = tid >> 1, kc = (tid & 1) * 8;    // a [rows][k] tile: row, first k of this thread
-    const int sr = tid >> 4, sc = (tid & 15) * 8;   // a [k][columns] tile: k, first column
-    float ra[8], rb[NB][8];
+    // a [rows][k] tile: row (and every KR on) and first k of this thread
+    constexpr int KT = GM_K / 8, KR = 256 / KT;
+    const int kr = tid / KT, kc = (tid % KT) * 8;
+    // a [k][columns] tile: k (and every SR on) and first column
+    constexpr int ST = GM_T / 8, SR = 256 / ST;
+    const int sr = tid / ST, sc = (tid % ST) * 8;
+    float ra[GM_H][8], rb[NB][GM_H][8];
     auto load = [&](int seg, int k0) {
         const TA* A = g.a[LAYOUT == GM_TN ? sel : seg];
-        if constexpr (LAYOUT == GM_TN) {
-            const int r = k0 + sr;
-            gm_load8<TA, VA>(ra, A + (size_t)r * g.lda + m0 + sc, r < k_end ? g.M - m0 - sc : 0);
-        } else {
-            const int r = m0 + kr;
-            gm_load8<TA, VA>(ra, A + (size_t)r * g.lda + k0 + kc, r < m_end ? k_end - k0 - kc : 0);
-        }
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const TB* B = g.b[DUAL ? i : (LAYOUT == GM_TN ? 0 : seg)];
-            if constexpr (LAYOUT == GM_NT) {
-                const int r = n0 + kr;
-                gm_load8<TB, VB>(rb[i], B + e * g.b_stride + (size_t)r * g.ldb + k0 + kc,
-                                 r < g.N ? k_end - k0 - kc : 0);
+        for (int h = 0; h < GM_H; ++h) {
+            if constexpr (LAYOUT == GM_TN) {
+                const int r = k0 + sr + SR * h;
+                gm_load8<TA, VA>(ra[h], A + (size_t)r * g.lda + m0 + sc, r < k_end ? g.M - m0 - sc : 0);
             } else {
-                const int r = k0 + sr;
-                gm_load8<TB, VB>(rb[i],
-                                 B + (LAYOUT == GM_TN ? 0 : e * g.b_stride) + (size_t)r * g.ldb + n0 + sc,
-                                 r < k_end ? g.N - n0 - sc : 0);
+                const int r = m0 + kr + KR * h;
+                gm_load8<TA, VA>(ra[h], A + (size_t)r * g.lda + k0 + kc, r < m_end ? k_end - k0 - kc : 0);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const TB* B = g.b[DUAL ? i : (LAYOUT == GM_TN ? 0 : seg)];
+                if constexpr (LAYOUT == GM_NT) {
+                    const int r = n0 + kr + KR * h;
+                    gm_load8<TB, VB>(rb[i][h], B + e * g.b_stride + (size_t)r * g.ldb + k0 + kc,
+                                     r < g.N ? k_end - k0 - kc : 0);
+                } else {
+                    const int r = k0 + sr + SR * h;
+                    gm_load8<TB, VB>(rb[i][h],
+                                     B + (LAYOUT == GM_TN ? 0 : e * g.b_stride) + (size_t)r * g.ldb + n0 + sc,
+                                     r < k_end ? g.N - n0 - sc : 0);
+                }
             }
         }
     };
-    auto store_rows = [&](float (&s)[GM_K][GM_LD], const float (&r)[8]) {
+    auto store_rows = [&](float (&s)[GM_K][GM_LD], const float (&r)[GM_H][8]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[kc + j][kr] = r[j];
+        for (int h = 0; h < GM_H; ++h)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[kc + j][kr + KR * h] = r[h][j];
     };
-    auto store_cols = [&](float (&s)[GM_K][GM_LD], const float (&r)[8]) {
-        *reinterpret_cast<f32x4*>(&s[sr][sc]) = f32x4{r[0], r[1], r[2], r[3]};
-        *reinterpret_cast<f32x4*>(&s[sr][sc + 4]) = f32x4{r[4], r[5], r[6], r[7]};
+    auto store_cols = [&](float (&s)[GM_K][GM_LD], const float (&r)[GM_H][8]) {
+#pragma unroll
+        for (int h = 0; h < GM_H; ++h) {
+            *reinterpret_cast<f32x4*>(&s[sr + SR * h][sc]) = f32x4{r[h][0], r[h][1], r[h][2], r[h][3]};
+            *reinterpret_cast<f32x4*>(&s[sr + SR * h][sc + 4]) = f32x4{r[h][4], r[h][5], r[h][6], r[h][7]};
+        }
     };
 
-    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+    const int wm = (wave & 1) * (GM_T / 2), wn = (wave >> 1) * (GM_T / 2);
     const int fr = lane & 31, fk = lane >> 5;
-    f32x16 acc[NB][2][2];
+    f32x16 acc[NB][BL][BL];
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+        for (int a = 0; a < BL; ++a)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < BL; ++b)
 #pragma unroll
                 for (int q = 0; q < 16; ++q) acc[i][a][b][q] = 0.0f;
 
@@ -173,24 +191,27 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi e
         }
 #pragma unroll
         for (int k = 0; k < GM_K; k += 2) {
-            const float a0 = sA[k + fk][wm + fr], a1 = sA[k + fk][wm + 32 + fr];
+            float a[BL];
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const float b0 = sB[i][k + fk][wn + fr], b1 = sB[i][k + fk][wn + 32 + fr];
-                acc[i][0][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a0, acc[i][0][0], 0, 0, 0);
-                acc[i][0][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a1, acc[i][0][1], 0, 0, 0);
-                acc[i][1][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a0, acc[i][1][0], 0, 0, 0);
-                acc[i][1][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a1, acc[i][1][1], 0, 0, 0);
-            }
+            for (int mb = 0; mb < BL; ++mb) a[mb] = sA[k + fk][wm + mb * 32 + fr];
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int nb = 0; nb < BL; ++nb) {
+                    const float b = sB[i][k + fk][wn + nb * 32 + fr];
+#pragma unroll
+                    for (int mb = 0; mb < BL; ++mb)
+                        acc[i][nb][mb] = __builtin_amdgcn_mfma_f32_32x32x2f32(b, a[mb], acc[i][nb][mb], 0, 0, 0);
+                }
         }
     }
     // element i of block (nb, mb): column 8 (i / 4) + 4 (lane / 32) + i % 4, row lane % 32
 #pragma unroll
-    for (int mb = 0; mb < 2; ++mb) {
+    for (int mb = 0; mb < BL; ++mb) {
         const int m = m0 + wm + mb * 32 + fr;
         if (m >= m_end) continue;
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
+        for (int nb = 0; nb < BL; ++nb)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int n = n0 + wn + nb * 32 + 8 * q + 4 * fk;

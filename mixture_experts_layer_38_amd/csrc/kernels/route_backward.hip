@@ -207,10 +207,18 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
                                                       const bf16* __restrict__ wr, const bf16* __restrict__ rows,
                                                       const int32_t* __restrict__ assign_row, bf16* __restrict__ dx) {
     __shared__ __align__(16) float sP[RX_T * RX_C];
+    __shared__ int32_t sRow[RX_T * 32];  // the tokens' grouped rows (K is at most 32)
     bf16* const sH = reinterpret_cast<bf16*>(sP);  // before sP is filled
     bf16* const sL = sH + RX_T * RX_LD;
-    const int t0 = blockIdx.x * RX_T, c0 = blockIdx.y * RX_C;
+    // column tiles first: the tokens' grouped rows are read whole at about the
+    // same time (token tiles first, in pieces of 256 bytes, took 190 us
+    // instead of 183)
+    const unsigned tc = (d + RX_C - 1) / RX_C;
+    const int t0 = blockIdx.x / tc * RX_T, c0 = blockIdx.x % tc * RX_C;
     const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+    if (rows != nullptr)
+        for (int i = tid; i < RX_T * K; i += 256)
+            sRow[i] = t0 + i / K < T ? assign_row[(size_t)t0 * K + i] : -1;
     const int fr = lane & 31, fk = (lane >> 5) * 8;
     f32x16 acc[2];
 #pragma unroll
@@ -273,7 +281,7 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
         const f32x4 a = *reinterpret_cast<const f32x4*>(sP + tl * RX_C + ((ch ^ (tl & 31)) << 2));
         const f32x4 b = *reinterpret_cast<const f32x4*>(sP + tl * RX_C + (((ch + 1) ^ (tl & 31)) << 2));
         float sum[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        if (rows != nullptr) add_rows(sum, rows, assign_row + (size_t)t * K, K, T * K, d, c);
+        if (rows != nullptr) add_rows(sum, rows, sRow + tl * K, K, T * K, d, c);
         bf16x8 o;
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = (bf16)sum[j];
@@ -382,7 +390,7 @@ __global__ __launch_bounds__(256) void route_dw_kernel(int T, int d, int E, cons
 // which all run at once (five parts instead of four on 112 tiles, 560
 // workgroups: 83 us), at least 128 tokens each.
 int dw_parts(int T, int d, int E) {
-    const int tiles = ((d + GM_T - 1) / GM_T) * ((E + GM_T - 1) / GM_T);
+    const int tiles = ((d + 127) / 128) * ((E + 127) / 128);
     return std::max(1, std::min(512 / tiles, (T + 127) / 128));
 }
 
@@ -390,12 +398,20 @@ template <bool VEC>
 hipError_t route_products(int n_tok, int d, int E, int K, const float* x, const float* wr, const float* dx_perm,
                           const int32_t* assign_row, const float* dl, float* dx, float* dwr, float* part, int parts,
                           hipStream_t s) {
-    const unsigned td = (d + GM_T - 1) / GM_T;
+    const auto tiles = [](int v, int t) { return (unsigned)((v + t - 1) / t); };
+    const auto with_tile = [](int tile, auto f) {
+        return tile == 64 ? f(std::integral_constant<int, 64>{}) : f(std::integral_constant<int, 128>{});
+    };
     hipError_t err;
     if (dx != nullptr) {
         GemmArgs<float, float> g{{dl, nullptr}, {wr, nullptr}, E, E, 0, 0, d, E, n_tok, 1, RowPlan{}, nullptr};
-        gemm_f32_kernel<GM_NT, false, 1, VEC, VEC><<<dim3((n_tok + GM_T - 1) / GM_T, td), 256, 0, s>>>(g, EpiProduct{dx});
-        if ((err = hipGetLastError()) != hipSuccess) return err;
+        err = with_tile(gm_tile((long)tiles(n_tok, 128) * tiles(d, 128)), [&](auto t) {
+            constexpr int T = decltype(t)::value;
+            gemm_f32_kernel<T, GM_NT, false, 1, VEC, VEC><<<dim3(tiles(n_tok, T), tiles(d, T)), 256, 0, s>>>(g,
+                                                                                                         EpiProduct{dx});
+            return hipGetLastError();
+        });
+        if (err != hipSuccess) return err;
         if (dx_perm != nullptr) {
             const size_t vecs = (size_t)n_tok * d / 8;
             route_add_rows_kernel<<<(unsigned)std::min<size_t>((vecs + 255) / 256, 1 << 20), 256, 0, s>>>(
@@ -405,9 +421,14 @@ hipError_t route_products(int n_tok, int d, int E, int K, const float* x, const 
     }
     if (dwr != nullptr) {
         GemmArgs<float, float> g{{x, nullptr}, {dl, nullptr}, d, E, 0, d, E, 0, n_tok, 1, RowPlan{}, nullptr};
-        gemm_f32_kernel<GM_TN, false, 1, true, VEC><<<dim3((E + GM_T - 1) / GM_T, td, parts), 256, 0, s>>>(
-            g, EpiPart{part, d});
-        if ((err = hipGetLastError()) != hipSuccess) return err;
+        // (a tile of 64 also wastes less of itself on few experts)
+        err = with_tile(E <= 64 ? 64 : gm_tile((long)tiles(E, 128) * tiles(d, 128) * parts), [&](auto t) {
+            constexpr int T = decltype(t)::value;
+            gemm_f32_kernel<T, GM_TN, false, 1, true, VEC><<<dim3(tiles(E, T), tiles(d, T), parts), 256, 0, s>>>(
+                g, EpiPart{part, d});
+            return hipGetLastError();
+        });
+        if (err != hipSuccess) return err;
     }
     return hipSuccess;
 }
@@ -418,7 +439,7 @@ hipError_t route_products(int n_tok, int d, int E, int K, const bf16* x, const b
                           hipStream_t s) {
     hipError_t err;
     if (dx != nullptr) {
-        route_dx_kernel<VEC><<<dim3((n_tok + RX_T - 1) / RX_T, (d + RX_C - 1) / RX_C), 256, 0, s>>>(
+        route_dx_kernel<VEC><<<(unsigned)((n_tok + RX_T - 1) / RX_T) * ((d + RX_C - 1) / RX_C), 256, 0, s>>>(
             n_tok, d, E, K, dl, wr, dx_perm, assign_row, dx);
         if ((err = hipGetLastError()) != hipSuccess) return err;
     }
