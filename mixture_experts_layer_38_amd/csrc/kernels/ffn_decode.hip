@@ -47,6 +47,7 @@ __device__ __forceinline__ u32x4 load16_masked(const bf16* row, int k, int K) {
 // from A row rowmap[r * topk] as is, or as zeros when that entry is negative
 // (the slots of a concatenation); otherwise row r is A row
 // rowmap[r] / topk (rowmap NULL: row r).
+// With PfKeep the gate and up sums are stored too, rounded to bf16.
 // With PfScales the rows hold 8-bit integers, two to a unit of K, lda and ldw:
 // the same loads feed v_mfma_i32_16x16x64_i8, and the epilogue scales the sums.
 template <bool GATED, int CPI, int NCB, bool ALIGNED, int R, bool PART = false, bool ZNEG = false, typename... X>
@@ -54,7 +55,7 @@ __device__ __forceinline__ void ffn_decode_group(
     int e, int n_rows, int N, int K, const bf16* __restrict__ A, const int32_t* __restrict__ rowmap, int topk,
     const int32_t* __restrict__ offsets, const bf16* __restrict__ Wa, const bf16* __restrict__ Wb,
     bf16* __restrict__ out, int lda, int ldw, float* __restrict__ part = nullptr, X... extra) {
-    constexpr bool I8 = pf_int8<X...>;
+    constexpr bool I8 = pf_int8<X...>, KEEP = pf_keeps<X...>;
     typedef typename std::conditional<I8, i32x4, f32x4>::type Acc;
     typedef typename std::conditional<I8, int32_t, float>::type Sum;
     constexpr int NG = GATED ? 2 : 1;
@@ -192,7 +193,7 @@ __device__ __forceinline__ void ffn_decode_group(
                     if (cb >= ncb) break;
                     // lane holds output (weight row 4g + i of block r, token column rl)
                     const int tcol = cb * 16 + rl;
-                    float v[4];
+                    float v[4], vg[4], vu[4];
                     float rs = 0.0f;
                     f32x4 wsa, wsb;
                     if constexpr (I8) {  // N is a multiple of 16
@@ -216,6 +217,21 @@ __device__ __forceinline__ void ffn_decode_group(
                             v[i] = GATED ? silu(f0) * ((float)s1 * rs * wsb[i]) : f0;
                         } else {
                             v[i] = GATED ? silu(s0) * s1 : s0;
+                        }
+                        if constexpr (KEEP) {
+                            vg[i] = s0;
+                            vu[i] = s1;
+                        }
+                    }
+                    if constexpr (KEEP) {  // N is a multiple of 8
+                        const PfKeep keep = pf_extra<PfKeep>(extra...);
+                        const int col = n0 + DC_ROWS * r + g * 4;
+                        if (tcol < mp && col < N) {
+                            const size_t at = (size_t)(r0 + p0 + tcol) * N + col;
+                            *reinterpret_cast<bf16x4*>(keep.gate + at) =
+                                bf16x4{(bf16)vg[0], (bf16)vg[1], (bf16)vg[2], (bf16)vg[3]};
+                            *reinterpret_cast<bf16x4*>(keep.up + at) =
+                                bf16x4{(bf16)vu[0], (bf16)vu[1], (bf16)vu[2], (bf16)vu[3]};
                         }
                     }
                     if (PART && tcol < mp) {
@@ -272,6 +288,21 @@ __global__ __launch_bounds__(DC_WAVES * kWave) void ffn_decode_expert_kernel(
         ffn_decode_group<GATED, CPI2, 2, ALIGNED, R>(e, n_rows, N, K, A, rowmap, topk, offsets, Wa, Wb, out, K, K);
     else
         ffn_decode_group<GATED, 1, 4, ALIGNED, R>(e, n_rows, N, K, A, rowmap, topk, offsets, Wa, Wb, out, K, K);
+}
+
+// The gate/up GEMM that keeps its projections.
+template <int CPI1, bool ALIGNED>
+__global__ __launch_bounds__(DC_WAVES * kWave) void ffn_decode_keep_kernel(
+    int n_rows, int N, int K, const bf16* __restrict__ A, const int32_t* __restrict__ offsets,
+    const bf16* __restrict__ Wa, const bf16* __restrict__ Wb, bf16* __restrict__ out, PfKeep keep) {
+    const int e = blockIdx.y;
+    const int m = min(offsets[e + 1], n_rows) - offsets[e];
+    if (m <= DC_ROWS)
+        ffn_decode_group<true, CPI1, 1, ALIGNED, 1, false, false, PfKeep>(e, n_rows, N, K, A, nullptr, 1, offsets, Wa,
+                                                                          Wb, out, K, K, nullptr, keep);
+    else
+        ffn_decode_group<true, 1, 2, ALIGNED, 1, false, false, PfKeep>(e, n_rows, N, K, A, nullptr, 1, offsets, Wa, Wb,
+                                                                       out, K, K, nullptr, keep);
 }
 
 // The same on 8-bit rows and weights (K: units of two values; rows of A padded
@@ -561,6 +592,26 @@ hipError_t launch_concat_small(int T, int Ks, int d, const void* h, const int32_
     const int n = T * d;
     linear_part_reduce_kernel<<<std::max(1, std::min((n + 255) / 256, 1024)), 256, 0, s>>>(n, parts, part,
                                                                                           (bf16*)y);
+    return hipGetLastError();
+}
+
+// The training pass of a decode-sized batch: launch_decode_t's GEMMs, gate and up kept.
+hipError_t launch_decode_keep(int n_rows, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
+                              const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act, bf16* h, hipStream_t s) {
+    const dim3 g1((F + DC_ROWS - 1) / DC_ROWS, E), g2((d + 4 * DC_ROWS - 1) / (4 * DC_ROWS), E);
+    const PfKeep keep{gate, up};
+    if (d % (2 * DC_KCH) == 0)
+        ffn_decode_keep_kernel<2, true><<<g1, DC_WAVES * kWave, 0, s>>>(n_rows, F, d, x, offsets, w1, w3, act, keep);
+    else
+        ffn_decode_keep_kernel<1, false><<<g1, DC_WAVES * kWave, 0, s>>>(n_rows, F, d, x, offsets, w1, w3, act, keep);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    if (F % (2 * DC_KCH) == 0)
+        ffn_decode_expert_kernel<false, 2, 2, true, 4><<<g2, DC_WAVES * kWave, 0, s>>>(n_rows, d, F, act, nullptr, 1,
+                                                                                      offsets, w2, nullptr, h);
+    else
+        ffn_decode_expert_kernel<false, 1, 1, false, 4><<<g2, DC_WAVES * kWave, 0, s>>>(n_rows, d, F, act, nullptr, 1,
+                                                                                       offsets, w2, nullptr, h);
     return hipGetLastError();
 }
 

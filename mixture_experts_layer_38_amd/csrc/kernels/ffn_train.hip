@@ -20,6 +20,8 @@ size_t prefill_ws_bytes(int n_rows, int E, int d);
 hipError_t launch_ffn_prefill_keep(int n_rows, int E, int d, int F, const bf16* x, const int32_t* offsets,
                                    const bf16* w1, const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act,
                                    bf16* h, void* ws, hipStream_t s);
+hipError_t launch_decode_keep(int n_rows, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
+                              const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act, bf16* h, hipStream_t s);
 
 hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
                            const bf16* w3, const bf16* w2, const bf16* gate, const bf16* up, const bf16* dh, bf16* dx,
@@ -163,6 +165,9 @@ hipError_t launch_ffn_train(int T, int K, int E, int d, int F, int dtype, const 
         if ((err = launch_row_plan(n, E, tile, offsets, rest, &plan, s)) != hipSuccess) return err;
         err = train_gemms(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3, (const float*)w2,
                           (float*)gate, (float*)up, (float*)base, (float*)h, tile, plan, s);
+    } else if (T <= 64) {  // the forward pass's choice: few rows per expert, bound by the weights
+        err = launch_decode_keep(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3, (const bf16*)w2,
+                                 (bf16*)gate, (bf16*)up, (bf16*)base, (bf16*)h, s);
     } else {
         err = launch_ffn_prefill_keep(n, E, d, F, (const bf16*)x, offsets, (const bf16*)w1, (const bf16*)w3,
                                       (const bf16*)w2, (bf16*)gate, (bf16*)up, (bf16*)base, (bf16*)h, rest, s);
