@@ -920,13 +920,13 @@ constexpr size_t PG_LDS_BYTES = 4 * PG_TILE_ELEMS * sizeof(bf16);
 // Generic variant for any K (a multiple of 8): the same tiles, with operands
 // staged HBM/L2 -> registers -> LDS (rows padded to 144 bytes), double
 // buffered with one 64-wide k step in flight.  N, K, n_nt as above.
-template <bool GATED, typename... X>
+template <bool GATED>
 __global__ __launch_bounds__(PG_THREADS) void ffn_prefill_generic_kernel(
     int n_rows, int N, int K, int n_nt, const bf16* __restrict__ A,
     const int32_t* __restrict__ rowmap, int topk, const int32_t* __restrict__ mt_count,
     const int32_t* __restrict__ mt_expert, const int32_t* __restrict__ mt_row0,
     const int32_t* __restrict__ offsets, const bf16* __restrict__ Wa, const bf16* __restrict__ Wb,
-    bf16* __restrict__ out, X... extra) {
+    bf16* __restrict__ out) {
     extern __shared__ __align__(16) bf16 smem[];
     const int n_mt = *mt_count;
     const int tiles = n_mt * n_nt;
@@ -1047,16 +1047,6 @@ __global__ __launch_bounds__(PG_THREADS) void ffn_prefill_generic_kernel(
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         v[r] = silu(acc[2 * pr][tb][4 * q + r]) * acc[2 * pr + 1][tb][4 * q + r];
-                    if constexpr (pf_keeps<X...>) {  // N is a multiple of 8
-                        const PfKeep keep = pf_extra<PfKeep>(extra...);
-                        const f32x16 &ga = acc[2 * pr][tb], &ua = acc[2 * pr + 1][tb];
-                        if (f < N) {
-                            *reinterpret_cast<bf16x4*>(keep.gate + (size_t)grow * N + f) =
-                                bf16x4{(bf16)ga[4 * q], (bf16)ga[4 * q + 1], (bf16)ga[4 * q + 2], (bf16)ga[4 * q + 3]};
-                            *reinterpret_cast<bf16x4*>(keep.up + (size_t)grow * N + f) =
-                                bf16x4{(bf16)ua[4 * q], (bf16)ua[4 * q + 1], (bf16)ua[4 * q + 2], (bf16)ua[4 * q + 3]};
-                        }
-                    }
                     if (f + 3 < N) {
                         bf16x4 pk = {(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
                         *reinterpret_cast<bf16x4*>(orow + f) = pk;
@@ -1188,7 +1178,7 @@ hipError_t launch_row_plan(int n_rows, int E, int bm, const int32_t* offsets, vo
 // concurrent first calls from several threads are safe); a failure is kept
 // and returned by every later call on that device.
 constexpr int PG_MAX_DEVICES = 64;
-template <bool GATED, typename... X>
+template <bool GATED>
 static hipError_t generic_lds_attr() {
     static std::once_flag once[PG_MAX_DEVICES];
     static hipError_t result[PG_MAX_DEVICES];
@@ -1197,7 +1187,7 @@ static hipError_t generic_lds_attr() {
     if (err != hipSuccess) return err;
     if (dev < 0 || dev >= PG_MAX_DEVICES) return hipErrorInvalidDevice;
     std::call_once(once[dev], [dev] {
-        result[dev] = hipFuncSetAttribute((const void*)ffn_prefill_generic_kernel<GATED, X...>,
+        result[dev] = hipFuncSetAttribute((const void*)ffn_prefill_generic_kernel<GATED>,
                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)PG_LDS_BYTES);
     });
     return result[dev];
@@ -1263,13 +1253,14 @@ static hipError_t launch_prefill_gemm(int n_rows, int N, int K, int n_nt, int ma
         return hipGetLastError();
         }
     }
-    if constexpr (pf_int8<X...>) return hipErrorInvalidValue;
-    else {
+    if constexpr (pf_int8<X...> || pf_keeps<X...>) {
+        return hipErrorInvalidValue;  // their callers take such widths elsewhere
+    } else {
     const unsigned grid = (unsigned)((((long)max_mt * n_nt + PF_XCD - 1) / PF_XCD) * PF_XCD);
-    hipError_t aerr = generic_lds_attr<GATED, X...>();
+    hipError_t aerr = generic_lds_attr<GATED>();
     if (aerr != hipSuccess) return aerr;
-    ffn_prefill_generic_kernel<GATED, X...><<<grid, PG_THREADS, PG_LDS_BYTES, s>>>(
-        n_rows, N, K, n_nt, A, rowmap, topk, mt_count, mt_expert, mt_row0, offsets, Wa, Wb, out, extra...);
+    ffn_prefill_generic_kernel<GATED><<<grid, PG_THREADS, PG_LDS_BYTES, s>>>(
+        n_rows, N, K, n_nt, A, rowmap, topk, mt_count, mt_expert, mt_row0, offsets, Wa, Wb, out);
     return hipGetLastError();
     }
 }
@@ -1351,7 +1342,8 @@ static PfWs pf_ws(int n_rows, int E, void* ws) {
     return w;
 }
 
-// The training pass: every expert on the tiled GEMMs, gate and up kept.
+// The training pass (d and F multiples of 64): every expert on the tiled
+// GEMMs, gate and up kept.
 hipError_t launch_ffn_prefill_keep(int n_rows, int E, int d, int F, const bf16* x, const int32_t* offsets,
                                    const bf16* w1, const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act,
                                    bf16* h, void* ws, hipStream_t s) {

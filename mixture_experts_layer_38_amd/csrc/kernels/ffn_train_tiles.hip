@@ -1,9 +1,12 @@
-// The grouped products of the expert FFN's backward pass in bf16 (formulas:
-// ffn_train.hip).  Unlike the forward pass's, they have operands that are
-// contiguous across the reduction:
-//   GRAD_ACT  da = dh W2_e             rows [r][k] times [k][n]; epilogue: dgate, dup, act
-//   GRAD_X    dx = dgate W1_e + dup W3_e   two such products into one sum
-//   GRAD_W    dW = P^T Q               [r][m] times [r][n], the sum over the expert's rows
+// The grouped products of the expert FFN in training, in bf16 (formulas:
+// ffn_train.hip).  Most have operands that are contiguous across the reduction:
+//   TR_DACT  da = dh W2_e                 rows [r][k] times [k][n]; epilogue: dgate, dup, act
+//   TR_DX    dx = dgate W1_e + dup W3_e   two such products into one sum
+//   TR_DW    dW = P^T Q                   [r][m] times [r][n], the sum over the expert's rows
+// and for widths that the forward pass's tiled kernel does not take (no
+// multiples of 64)
+//   TR_GATE  gate, up = rows [r][k] times W1_e, W3_e [n][k]; epilogue: act as well
+//   TR_DOWN  h = act W2_e^T               the same with one weight
 //
 // Tiles of BM x 256 outputs on four waves (2 x 2), v_mfma_f32_32x32x16_bf16
 // with the n side as the first operand, so a lane ends with four consecutive
@@ -34,32 +37,33 @@ namespace moe {
 
 namespace {
 
-enum { GRAD_ACT, GRAD_X, GRAD_W };
-constexpr int GR_BN = 256;
-constexpr int GR_W_LONG = 512;
-constexpr int GR_GM = 8;  // row tiles per group in GRAD_W's order
+enum { TR_DACT, TR_DX, TR_DW, TR_GATE, TR_DOWN };
+constexpr int TR_BN = 256;
+constexpr int TR_DW_LONG = 512;
+constexpr int TR_GM = 8;  // row tiles per group in TR_DW's order
 
-struct GradArgs {
-    const bf16 *a0, *a1;  // rows (GRAD_X: of both products; GRAD_W: the m side of both results)
-    const bf16 *b0, *b1;  // the n side
+struct TrainArgs {
+    const bf16 *a0, *a1;  // rows (TR_DX: of both products; TR_DW: the m side of both results)
+    const bf16 *b0, *b1;  // the n side (TR_GATE: both weights)
     bf16 *out0, *out1, *out2;
     const bf16 *gate, *up;
     int n_rows, E;
-    int M, N, K;  // GRAD_W: results are [M][N]; else [rows][N], K the reduction of one product
+    int M, N, K;  // TR_DW: results are [M][N]; else [rows][N], K the reduction of one product
     int lda, ldb;
-    int n_mt, n_nt, sels;  // GRAD_W: row tiles per result, results per expert
+    int n_mt, n_nt, sels;  // TR_DW: row tiles per result, results per expert
     RowPlan plan;
     const int32_t* offsets;
 };
 
-// KT: K is not a multiple of the stage, so a row's chunks past it are masked
-// (rows of the next one otherwise; GRAD_W has no such rows).
+// KT: K is not a multiple of the stage, so a [r][k] row's chunks past it are
+// masked (they would be the next row's; TR_DW has no such rows).
 template <int MODE, int BM, bool KT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == 256 ? 1 : 2, BM == 256 ? 1 : 2)))
-void ffn_grad_kernel(GradArgs g) {
-    constexpr bool WG = MODE == GRAD_W;
-    constexpr int GR_BK = BM == 256 ? 64 : 32;  // k per stage
-    constexpr int SA = BM * GR_BK, SB = GR_BN * GR_BK;  // elements of a stage's halves
+void ffn_train_kernel(TrainArgs g) {
+    constexpr bool WG = MODE == TR_DW;
+    constexpr bool BROWS = MODE == TR_GATE || MODE == TR_DOWN;  // the n side lies in [n][k] rows
+    constexpr int TR_BK = BM == 256 ? 64 : 32;  // k per stage
+    constexpr int SA = BM * TR_BK, SB = TR_BN * TR_BK;  // elements of a stage's halves
     constexpr int NTB = BM / 64;   // 32-wide m blocks per wave
     constexpr int NJA = SA / 2048, NJB = SB / 2048, NLD = NJA + NJB;  // loads per wave and stage
     constexpr bool RING5 = BM == 256;
@@ -87,10 +91,10 @@ void ffn_grad_kernel(GradArgs g) {
             A0 = g.a1;
             out = g.out1;
         }
-        const int grp = t / (GR_GM * g.n_nt), gsize = min(GR_GM, g.n_mt - grp * GR_GM);
-        const int rem = t - grp * GR_GM * g.n_nt;
-        m0 = __builtin_amdgcn_readfirstlane((grp * GR_GM + rem % gsize) * BM);
-        n0 = __builtin_amdgcn_readfirstlane(rem / gsize * GR_BN);
+        const int grp = t / (TR_GM * g.n_nt), gsize = min(TR_GM, g.n_mt - grp * TR_GM);
+        const int rem = t - grp * TR_GM * g.n_nt;
+        m0 = __builtin_amdgcn_readfirstlane((grp * TR_GM + rem % gsize) * BM);
+        n0 = __builtin_amdgcn_readfirstlane(rem / gsize * TR_BN);
         k_beg = __builtin_amdgcn_readfirstlane(min(max(g.offsets[e], 0), g.n_rows));
         k_len = max(__builtin_amdgcn_readfirstlane(min(g.offsets[e + 1], g.n_rows)) - k_beg, 0);
         out += (size_t)e * g.M * g.N;
@@ -104,22 +108,38 @@ void ffn_grad_kernel(GradArgs g) {
         e = tl.e;
         row0 = tl.row0;
         row_end = min(tl.row_end, row0 + BM);
-        n0 = tl.nt * GR_BN;
+        n0 = tl.nt * (MODE == TR_GATE ? 128 : TR_BN);
         const size_t we = (size_t)e * g.K * g.N;
         B0 += we;
-        if (MODE == GRAD_X) B1 += we;
+        if (MODE == TR_DX || MODE == TR_GATE) B1 += we;
     }
-    const int nk1 = (k_len + GR_BK - 1) / GR_BK;  // stages of one product
-    const int nk = MODE == GRAD_X ? 2 * nk1 : nk1;
+    const int nk1 = (k_len + TR_BK - 1) / TR_BK;  // stages of one product
+    const int nk = MODE == TR_DX ? 2 * nk1 : nk1;
 
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
     const int lane = lane_id();
 
     // ---- loads -------------------------------------------------------------------
+    // [r][k] halves: instruction j of wave w fills rows 8 (w + 4 j) .. + 7 of 128
+    // bytes, whose swizzle depends on j's lowest bit, or rows 16 (w + 4 j) .. + 15
+    // of 64 bytes.  off[j & 1]: the lane's byte offset at j = 0 (rows `back` fewer),
+    // first[j & 1]: the first k of its chunk.
+    auto row_chunks = [&](int back, uint32_t (&off)[2], int (&first)[2], int ld) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (TR_BK == 32) {
+                first[i] = ((lane & 3) ^ ((lane >> 3) & 3)) * 8;
+                off[i] = (uint32_t)((16 * wave - back + (lane >> 2)) * ld + first[i]) * 2;
+            } else {
+                first[i] = ((lane & 7) ^ pf_swz(8 * (wave + 4 * i) + (lane >> 3))) * 8;
+                off[i] = (uint32_t)((8 * wave + (lane >> 3)) * ld + first[i]) * 2;
+            }
+        }
+    };
     // [k][n] halves: instruction j of wave w fills rows 2 (w + 4 j) and the next
     // ([k][m] with 128 m: four rows from 4 (w + 4 j)); lane p slot p % 32 (16).
     const int brow = 2 * wave + (lane >> 5);
-    const uint32_t vb = (uint32_t)(brow * g.ldb + ((lane & 31) ^ ((brow & 3) << 2)) * 8) * 2;
+    uint32_t vb[2] = {(uint32_t)(brow * g.ldb + ((lane & 31) ^ ((brow & 3) << 2)) * 8) * 2, 0};
     constexpr int ACH = BM / 8;           // chunks of a [k][m] row
     constexpr int ARI = kWave / ACH;      // rows of one instruction
     uint32_t va[2];
@@ -128,54 +148,68 @@ void ffn_grad_kernel(GradArgs g) {
         const int arow = ARI * wave + lane / ACH;
         va[0] = va[1] = (uint32_t)(arow * g.lda + ((lane % ACH) ^ ((arow & 3) << 2)) * 8) * 2;
         ac[0] = ac[1] = 0;
-    } else if constexpr (GR_BK == 32) {
-        // [r][k] of 64-byte rows: instruction j of wave w fills rows 16 (w + 4 j) .. + 15
-        ac[0] = ac[1] = ((lane & 3) ^ ((lane >> 3) & 3)) * 8;
-        va[0] = va[1] = (uint32_t)((16 * wave + (lane >> 2)) * g.lda + ac[0]) * 2;
     } else {
-        // [r][k] of 128-byte rows: instruction j of wave w fills rows
-        // 8 (w + 4 j) .. + 7, whose swizzle depends on j's lowest bit
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int tr = 8 * (wave + 4 * i) + (lane >> 3);
-            ac[i] = ((lane & 7) ^ pf_swz(tr)) * 8;  // first k of the lane's chunk
-            va[i] = (uint32_t)((8 * wave + (lane >> 3)) * g.lda + ac[i]) * 2;
-        }
+        row_chunks(0, va, ac, g.lda);
     }
+    // [n][k] halves: as [r][k] ones, of 256 weight rows.  TR_GATE: 128 rows of
+    // each weight in alternating blocks of 32, so a lane's gate and up sums meet;
+    // a wave instruction then fetches rows of one weight: with 64 k a stage, of
+    // W1 for even j and W3 for odd, with 32, of W1 in waves 0 and 1.
+    int bc[2] = {0, 0};
+    if constexpr (BROWS) row_chunks(MODE == TR_GATE && TR_BK == 32 ? 16 * (wave & 2) : 0, vb, bc, g.ldb);
     // Descriptors of stage kt: its first element and the bytes from there on that exist.
     auto rsrc = [&](const bf16* p, int bytes) __attribute__((always_inline)) {
         return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000);
     };
     auto rs_a = [&](int kt) __attribute__((always_inline)) {
         if constexpr (WG) {
-            const int v = min(max(k_len - kt * GR_BK, 0), GR_BK);
-            return rsrc(A0 + (size_t)(k_beg + kt * GR_BK) * g.lda + m0, v > 0 ? (v * g.lda - m0) * 2 : 0);
+            const int v = min(max(k_len - kt * TR_BK, 0), TR_BK);
+            return rsrc(A0 + (size_t)(k_beg + kt * TR_BK) * g.lda + m0, v > 0 ? (v * g.lda - m0) * 2 : 0);
         } else {
-            const int seg = MODE == GRAD_X && kt >= nk1;
-            const int k0 = (kt - (seg ? nk1 : 0)) * GR_BK;
+            const int seg = MODE == TR_DX && kt >= nk1;
+            const int k0 = (kt - (seg ? nk1 : 0)) * TR_BK;
             const int bytes = kt < nk ? ((row_end - row0) * g.lda - k0) * 2 : 0;
             return rsrc((seg ? A1 : A0) + (size_t)row0 * g.lda + k0, bytes);
         }
     };
-    auto rs_b = [&](int kt) __attribute__((always_inline)) {
-        const int seg = MODE == GRAD_X && kt >= nk1;
-        const int k0 = (kt - (seg ? nk1 : 0)) * GR_BK;
-        const int v = kt < nk ? min(k_len - k0, GR_BK) : 0;
+    auto rs_b = [&](int kt, int which = 0) __attribute__((always_inline)) {
+        if constexpr (BROWS) {
+            const int bytes = kt < nk ? (min(g.N - n0, MODE == TR_GATE ? 128 : TR_BN) * g.ldb - kt * TR_BK) * 2 : 0;
+            return rsrc((which ? B1 : B0) + (size_t)n0 * g.ldb + kt * TR_BK, bytes);
+        }
+        const int seg = MODE == TR_DX && kt >= nk1;
+        const int k0 = (kt - (seg ? nk1 : 0)) * TR_BK;
+        const int v = kt < nk ? min(k_len - k0, TR_BK) : 0;
         return rsrc((seg ? B1 : B0) + (size_t)(k_beg + k0) * g.ldb + n0, v > 0 ? (v * g.ldb - n0) * 2 : 0);
     };
     auto ld_a = [&](__amdgpu_buffer_rsrc_t r, int kt, int j, bf16* dst) __attribute__((always_inline)) {
         uint32_t v = va[j & 1];
         if constexpr (KT && !WG) {
-            const int k0 = (kt - (MODE == GRAD_X && kt >= nk1 ? nk1 : 0)) * GR_BK;
-            v = ac[j & 1] < k_len - k0 ? v : 0x80000000u;
+            const int k0 = (kt - (MODE == TR_DX && kt >= nk1 ? nk1 : 0)) * TR_BK;
+            v = ac[j & 1] < k_len - k0 ? v : 0x80000000u;  // past every descriptor's bytes
         }
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             r, (__attribute__((address_space(3))) void*)(dst + (wave + 4 * j) * 512), 16, v,
-            WG ? j * (4 * ARI * 2) * g.lda : j * (4096 / GR_BK) * g.lda, 0, 0);
+            WG ? j * (4 * ARI * 2) * g.lda : j * (4096 / TR_BK) * g.lda, 0, 0);
     };
-    auto ld_b = [&](__amdgpu_buffer_rsrc_t r, int j, bf16* dst) __attribute__((always_inline)) {
+    auto ld_b = [&](const __amdgpu_buffer_rsrc_t (&r)[2], int kt, int j, bf16* dst) __attribute__((always_inline)) {
+        uint32_t v = vb[BROWS ? j & 1 : 0];
+        if constexpr (KT && BROWS) v = bc[j & 1] < k_len - kt * TR_BK ? v : 0x80000000u;
+        // rows that a step of j moves on by
+        constexpr int JR = !BROWS ? 8 : 4096 / TR_BK / 2 / (MODE == TR_GATE && TR_BK == 32 ? 2 : 1);
+        const int rows = MODE == TR_GATE && TR_BK == 64 ? (j >> 1) * JR : j * JR;
+        const int which = MODE != TR_GATE ? 0 : TR_BK == 64 ? j & 1 : 0;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            r, (__attribute__((address_space(3))) void*)(dst + (wave + 4 * j) * 512), 16, vb, j * 16 * g.ldb, 0, 0);
+            r[which], (__attribute__((address_space(3))) void*)(dst + (wave + 4 * j) * 512), 16, v, rows * 2 * g.ldb, 0, 0);
+    };
+    // The weights' descriptors of stage kt (TR_GATE with 32 k a stage: each wave's own weight).
+    struct RsB {
+        __amdgpu_buffer_rsrc_t r[2];
+    };
+    auto rs_bs = [&](int kt) __attribute__((always_inline)) {
+        if constexpr (MODE == TR_GATE && TR_BK == 64) return RsB{{rs_b(kt, 0), rs_b(kt, 1)}};
+        else if constexpr (MODE == TR_GATE) return RsB{{rs_b(kt, wave >> 1), rs_b(kt, wave >> 1)}};
+        else return RsB{{rs_b(kt), rs_b(kt)}};
     };
 
     // ---- fragments ------------------------------------------------------------------
@@ -185,28 +219,38 @@ void ffn_grad_kernel(GradArgs g) {
     int boff[4], aoff[NTB];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        boff[i] = (8 * fhalf + rr) * GR_BN + (((16 * wn + 4 * i + 2 * g16 + (cc >> 1)) ^ (rr << 2)) << 3) + (cc & 1) * 4;
+        boff[i] = BROWS ? (wn * 128 + i * 32 + (lane & 31)) * TR_BK :
+                  (8 * fhalf + rr) * TR_BN + (((16 * wn + 4 * i + 2 * g16 + (cc >> 1)) ^ (rr << 2)) << 3) + (cc & 1) * 4;
 #pragma unroll
     for (int i = 0; i < NTB; ++i) {
         if constexpr (WG)
             aoff[i] = (8 * fhalf + rr) * BM + (((4 * NTB * wm + 4 * i + 2 * g16 + (cc >> 1)) ^ (rr << 2)) << 3) +
                       (cc & 1) * 4;
         else
-            aoff[i] = (wm * (BM / 2) + i * 32 + (lane & 31)) * GR_BK;
+            aoff[i] = (wm * (BM / 2) + i * 32 + (lane & 31)) * TR_BK;
     }
-    int asw[NTB];
+    int asw[NTB], bsw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = wn * 128 + i * 32 + (lane & 31);
+        bsw[i] = TR_BK == 32 ? (r >> 1) & 3 : pf_swz(r);
+    }
 #pragma unroll
     for (int i = 0; i < NTB; ++i) {
         const int r = wm * (BM / 2) + i * 32 + (lane & 31);
-        asw[i] = GR_BK == 32 ? (r >> 1) & 3 : pf_swz(r);
+        asw[i] = TR_BK == 32 ? (r >> 1) & 3 : pf_swz(r);
     }
     struct Frags {
         bf16x8 n[4], m[NTB];
     };
     auto read = [&](const bf16* cA, const bf16* cB, int q, Frags& f) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f.n[i] = read_tr(cB + boff[i] + 16 * q * GR_BN, cB + boff[i] + (16 * q + 4) * GR_BN);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BROWS)
+                f.n[i] = *reinterpret_cast<const bf16x8*>(cB + boff[i] + ((2 * q + fhalf) ^ bsw[i]) * 8);
+            else
+                f.n[i] = read_tr(cB + boff[i] + 16 * q * TR_BN, cB + boff[i] + (16 * q + 4) * TR_BN);
+        }
 #pragma unroll
         for (int i = 0; i < NTB; ++i) {
             if constexpr (WG)
@@ -216,7 +260,7 @@ void ffn_grad_kernel(GradArgs g) {
         }
     };
     constexpr int NM = 4 * NTB;                       // MFMAs of a quarter
-    constexpr int NR = 8 + (WG ? 2 * NTB : NTB);      // LDS reads of a quarter
+    constexpr int NR = (BROWS ? 4 : 8) + (WG ? 2 * NTB : NTB);  // LDS reads of a quarter
     f32x16 acc[4][NTB];
 #pragma unroll
     for (int a = 0; a < 4; ++a)
@@ -252,7 +296,8 @@ void ffn_grad_kernel(GradArgs g) {
     Frags fa, fb;
     auto step5 = [&](int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA) __attribute__((always_inline)) {
         // A(kt + 2) into pA early, B(kt + 2) into A(kt)'s unit after the barrier
-        const auto ra = rs_a(kt + 2), rb = rs_b(kt + 2);
+        const auto ra = rs_a(kt + 2);
+        const RsB rb = rs_bs(kt + 2);
         read(cA, cB, 1, fb);
 #pragma unroll
         for (int j = 0; j < 3; ++j) ld_a(ra, kt + 2, j, pA);
@@ -276,7 +321,7 @@ void ffn_grad_kernel(GradArgs g) {
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < NJB; ++j) ld_b(rb, j, cA);
+        for (int j = 0; j < NJB; ++j) ld_b(rb.r, kt + 2, j, cA);
         read(nA, nB, 0, fa);
         mma(fb);
         weave(std::integral_constant<int, NJB>{});
@@ -286,12 +331,13 @@ void ffn_grad_kernel(GradArgs g) {
     // stage's two 16-wide parts.
     auto step3 = [&](int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA, bf16* pB) __attribute__((always_inline)) {
         constexpr int V = NLD / 2;
-        const auto ra = rs_a(kt + 2), rb = rs_b(kt + 2);
+        const auto ra = rs_a(kt + 2);
+        const RsB rb = rs_bs(kt + 2);
         auto lds = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = i0; i < i0 + V; ++i) {
                 if (i < NJA) ld_a(ra, kt + 2, i, pA);
-                else ld_b(rb, i - NJA, pB);
+                else ld_b(rb.r, kt + 2, i - NJA, pB);
             }
         };
         read(cA, cB, 1, fb);
@@ -310,11 +356,12 @@ void ffn_grad_kernel(GradArgs g) {
         __builtin_amdgcn_sched_barrier(0);
     };
     auto first = [&](int kt, bf16* dA, bf16* dB) __attribute__((always_inline)) {
-        const auto ra = rs_a(kt), rb = rs_b(kt);
+        const auto ra = rs_a(kt);
+        const RsB rb = rs_bs(kt);
 #pragma unroll
         for (int j = 0; j < NJA; ++j) ld_a(ra, kt, j, dA);
 #pragma unroll
-        for (int j = 0; j < NJB; ++j) ld_b(rb, j, dB);
+        for (int j = 0; j < NJB; ++j) ld_b(rb.r, kt, j, dB);
     };
     if (nk > 0) {
         if constexpr (RING5) {
@@ -366,7 +413,7 @@ void ffn_grad_kernel(GradArgs g) {
                            : (wave == 0 ? sB0 : wave == 1 ? sB1 : wave == 2 ? sB2 : sA0);
     const int mrow = wm * (BM / 2), ncol = n0 + wn * 128;
     const int el = pf_lane_fresh();
-    if constexpr (MODE == GRAD_ACT) {
+    if constexpr (MODE == TR_DACT) {
         // fp32 sums, 32 rows x 64 columns (8 KB) at a time; then gate and up by whole lines
         float* const sf = reinterpret_cast<float*>(st);
         const int lrow = el >> 3, lch = el & 7;  // eight chunks of eight columns per row
@@ -417,6 +464,37 @@ void ffn_grad_kernel(GradArgs g) {
                 }
             }
         }
+    } else if constexpr (MODE == TR_GATE) {
+        // blocks 0 and 2 hold gate sums, 1 and 3 the up sums of the same 32
+        // features: act, gate and up in turn, the wave's rows x 64 features each
+        const int lrow = el >> 3, lch = el & 7;
+        const int c = n0 + wn * 64 + lch * 8;
+#pragma unroll
+        for (int which = 0; which < 3; ++which) {
+            bf16* const dst = which == 0 ? g.out0 : which == 1 ? g.out1 : g.out2;
+#pragma unroll
+            for (int mb = 0; mb < NTB; ++mb)
+#pragma unroll
+                for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int rl = mb * 32 + (el & 31), cl = pr * 32 + 8 * q + 4 * (el >> 5);
+                        const f32x16 &ga = acc[2 * pr][mb], &ua = acc[2 * pr + 1][mb];
+                        bf16x4 o;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float gv = ga[4 * q + j], uv = ua[4 * q + j];
+                            o[j] = (bf16)(which == 0 ? silu(gv) * uv : which == 1 ? gv : uv);
+                        }
+                        *reinterpret_cast<bf16x4*>(st + rl * 64 + (((cl >> 3) ^ (rl & 7)) << 3) + (cl & 7)) = o;
+                    }
+#pragma unroll
+            for (int i = 0; i < NTB * 4; ++i) {
+                const int rl = i * 8 + lrow, r = row0 + mrow + rl;
+                const bf16x8 v = *reinterpret_cast<const bf16x8*>(st + rl * 64 + ((lch ^ (rl & 7)) << 3));
+                if (r < row_end && c < g.N) *reinterpret_cast<bf16x8*>(dst + (size_t)r * g.N + c) = v;
+            }
+        }
     } else {
         // in passes of the rows that a unit holds
         constexpr int PB = RING5 ? NTB : 1;  // 32-row blocks per pass
@@ -449,16 +527,16 @@ void ffn_grad_kernel(GradArgs g) {
 }
 
 template <int MODE, bool KT>
-hipError_t launch_grad(const GradArgs& g, int bm, unsigned grid, hipStream_t s) {
-    if (bm == 256) ffn_grad_kernel<MODE, 256, KT><<<grid, 256, 0, s>>>(g);
-    else ffn_grad_kernel<MODE, 128, KT><<<grid, 256, 0, s>>>(g);
+hipError_t launch_tiles(const TrainArgs& g, int bm, unsigned grid, hipStream_t s) {
+    if (bm == 256) ffn_train_kernel<MODE, 256, KT><<<grid, 256, 0, s>>>(g);
+    else ffn_train_kernel<MODE, 128, KT><<<grid, 256, 0, s>>>(g);
     return hipGetLastError();
 }
 
 // The result of P^T Q for every expert (and for a second P where a1 is given).
-hipError_t launch_grad_w(int n, int E, int M, int N, const bf16* p0, const bf16* p1, const bf16* q, bf16* out0,
+hipError_t launch_dw(int n, int E, int M, int N, const bf16* p0, const bf16* p1, const bf16* q, bf16* out0,
                          bf16* out1, const int32_t* offsets, hipStream_t s) {
-    GradArgs g{};
+    TrainArgs g{};
     g.a0 = p0;
     g.a1 = p1;
     g.b0 = q;
@@ -470,26 +548,62 @@ hipError_t launch_grad_w(int n, int E, int M, int N, const bf16* p0, const bf16*
     g.N = g.ldb = N;
     g.sels = p1 != nullptr ? 2 : 1;
     g.offsets = offsets;
-    const int bm = n >= GR_W_LONG * E ? 256 : 128;
+    const int bm = n >= TR_DW_LONG * E ? 256 : 128;
     g.n_mt = (M + bm - 1) / bm;
-    g.n_nt = (N + GR_BN - 1) / GR_BN;
+    g.n_nt = (N + TR_BN - 1) / TR_BN;
     const long per = ((long)g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD;
-    return launch_grad<GRAD_W, false>(g, bm, (unsigned)(per * E * g.sels * PF_XCD), s);
+    return launch_tiles<TR_DW, false>(g, bm, (unsigned)(per * E * g.sels * PF_XCD), s);
 }
 
 }  // namespace
+
+// Row tiles: 256 from 128 rows per expert on (padded halves cost little where
+// the weights are the bound: 32 experts of 128 rows, d 7168, F 2048: da 253 ->
+// 203 us, dx 507 -> 467), else 128.
+static int train_bm(int n, int E) { return n >= 128 * E ? 256 : 128; }
+static unsigned train_grid(int n, int E, int bm, int n_nt) {
+    return (unsigned)(((long)row_plan_tiles(n, E, bm) * n_nt + PF_XCD - 1) / PF_XCD * PF_XCD);
+}
+
+hipError_t launch_ffn_train_tiles(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
+                                  const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act, bf16* h, void* ws,
+                                  hipStream_t s) {
+    const int bm = train_bm(n, E);
+    TrainArgs g{};
+    hipError_t err = launch_row_plan(n, E, bm, offsets, ws, &g.plan, s);
+    if (err != hipSuccess) return err;
+    g.n_rows = n;
+    g.E = E;
+    g.offsets = offsets;
+    g.a0 = x;
+    g.b0 = w1;
+    g.b1 = w3;
+    g.out0 = act;
+    g.out1 = gate;
+    g.out2 = up;
+    g.N = F;
+    g.K = g.lda = g.ldb = d;
+    g.n_nt = (F + 127) / 128;
+    if ((err = launch_tiles<TR_GATE, true>(g, bm, train_grid(n, E, bm, g.n_nt), s)) != hipSuccess) return err;
+    g.a0 = act;
+    g.b0 = w2;
+    g.out0 = h;
+    g.N = d;
+    g.K = g.lda = g.ldb = F;
+    g.n_nt = (d + TR_BN - 1) / TR_BN;
+    return launch_tiles<TR_DOWN, true>(g, bm, train_grid(n, E, bm, g.n_nt), s);
+}
 
 hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
                            const bf16* w3, const bf16* w2, const bf16* gate, const bf16* up, const bf16* dh, bf16* dx,
                            bf16* dw1, bf16* dw3, bf16* dw2, bf16* dgate, bf16* dup, bf16* act, void* ws,
                            hipStream_t s) {
-    const int bm = n >= 128 * E ? 256 : 128;
+    const int bm = train_bm(n, E);
     RowPlan plan;
     hipError_t err = launch_row_plan(n, E, bm, offsets, ws, &plan, s);
     if (err != hipSuccess) return err;
-    const long mt = row_plan_tiles(n, E, bm);
-    auto grid = [&](int n_nt) { return (unsigned)((mt * n_nt + PF_XCD - 1) / PF_XCD * PF_XCD); };
-    GradArgs g{};
+    auto grid = [&](int n_nt) { return train_grid(n, E, bm, n_nt); };
+    TrainArgs g{};
     g.a0 = dh;
     g.b0 = w2;
     g.out0 = dgate;
@@ -501,15 +615,15 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
     g.E = E;
     g.N = g.ldb = F;
     g.K = g.lda = d;
-    g.n_nt = (F + GR_BN - 1) / GR_BN;
+    g.n_nt = (F + TR_BN - 1) / TR_BN;
     g.plan = plan;
     g.offsets = offsets;
-    err = d % 64 == 0 ? launch_grad<GRAD_ACT, false>(g, bm, grid(g.n_nt), s)
-                         : launch_grad<GRAD_ACT, true>(g, bm, grid(g.n_nt), s);
+    err = d % 64 == 0 ? launch_tiles<TR_DACT, false>(g, bm, grid(g.n_nt), s)
+                         : launch_tiles<TR_DACT, true>(g, bm, grid(g.n_nt), s);
     if (err != hipSuccess) return err;
     if (dw2 != nullptr) {
-        if ((err = launch_grad_w(n, E, d, F, dh, nullptr, act, dw2, nullptr, offsets, s)) != hipSuccess) return err;
-        if ((err = launch_grad_w(n, E, F, d, dgate, dup, x, dw1, dw3, offsets, s)) != hipSuccess) return err;
+        if ((err = launch_dw(n, E, d, F, dh, nullptr, act, dw2, nullptr, offsets, s)) != hipSuccess) return err;
+        if ((err = launch_dw(n, E, F, d, dgate, dup, x, dw1, dw3, offsets, s)) != hipSuccess) return err;
     }
     if (dx != nullptr) {
         g.a0 = dgate;
@@ -519,9 +633,9 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
         g.out0 = dx;
         g.N = g.ldb = d;
         g.K = g.lda = F;
-        g.n_nt = (d + GR_BN - 1) / GR_BN;
-        err = F % 64 == 0 ? launch_grad<GRAD_X, false>(g, bm, grid(g.n_nt), s)
-                             : launch_grad<GRAD_X, true>(g, bm, grid(g.n_nt), s);
+        g.n_nt = (d + TR_BN - 1) / TR_BN;
+        err = F % 64 == 0 ? launch_tiles<TR_DX, false>(g, bm, grid(g.n_nt), s)
+                             : launch_tiles<TR_DX, true>(g, bm, grid(g.n_nt), s);
     }
     return err;
 }

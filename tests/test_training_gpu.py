@@ -59,6 +59,10 @@ FFN_CASES = [
     (300, 1, 520, 1032, [300]),
     (70, 2, 64, 64, [2] * 70),
     (40, 2, 136, 72, [0, 0, 0]),
+    (200, 2, 72, 104, [50, 0, 100, 33, 64, 1, 90, 62]),
+    (500, 2, 136, 1000, [129, 300, 0, 31, 255]),
+    (90, 2, 128, 136, [0, 180]),
+    (64, 2, 264, 200, [33, 31, 64, 0]),
 ]
 
 
