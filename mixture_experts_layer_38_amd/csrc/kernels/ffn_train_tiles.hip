@@ -559,8 +559,11 @@ hipError_t launch_dw(int n, int E, int M, int N, const bf16* p0, const bf16* p1,
 
 // Row tiles: 256 from 128 rows per expert on (padded halves cost little where
 // the weights are the bound: 32 experts of 128 rows, d 7168, F 2048: da 253 ->
-// 203 us, dx 507 -> 467), else 128.
-static int train_bm(int n, int E) { return n >= 128 * E ? 256 : 128; }
+// 203 us, dx 507 -> 467), else 128, and 128 too where 256 would leave compute
+// units idle (cols: the narrower product's columns).
+static int train_bm(int n, int E, int cols) {
+    return n >= 128 * E && (long)row_plan_tiles(n, E, 256) * ((cols + TR_BN - 1) / TR_BN) >= 256 ? 256 : 128;
+}
 static unsigned train_grid(int n, int E, int bm, int n_nt) {
     return (unsigned)(((long)row_plan_tiles(n, E, bm) * n_nt + PF_XCD - 1) / PF_XCD * PF_XCD);
 }
@@ -568,7 +571,7 @@ static unsigned train_grid(int n, int E, int bm, int n_nt) {
 hipError_t launch_ffn_train_tiles(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
                                   const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act, bf16* h, void* ws,
                                   hipStream_t s) {
-    const int bm = train_bm(n, E);
+    const int bm = train_bm(n, E, std::min(d, F));
     TrainArgs g{};
     hipError_t err = launch_row_plan(n, E, bm, offsets, ws, &g.plan, s);
     if (err != hipSuccess) return err;
@@ -598,7 +601,7 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
                            const bf16* w3, const bf16* w2, const bf16* gate, const bf16* up, const bf16* dh, bf16* dx,
                            bf16* dw1, bf16* dw3, bf16* dw2, bf16* dgate, bf16* dup, bf16* act, void* ws,
                            hipStream_t s) {
-    const int bm = train_bm(n, E);
+    const int bm = train_bm(n, E, std::min(d, F));
     RowPlan plan;
     hipError_t err = launch_row_plan(n, E, bm, offsets, ws, &plan, s);
     if (err != hipSuccess) return err;
