@@ -98,6 +98,12 @@ void ffn_train_kernel(TrainArgs g) {
         k_beg = __builtin_amdgcn_readfirstlane(min(max(g.offsets[e], 0), g.n_rows));
         k_len = max(__builtin_amdgcn_readfirstlane(min(g.offsets[e + 1], g.n_rows)) - k_beg, 0);
         out += (size_t)e * g.M * g.N;
+        if (k_len == 0) {  // an expert without rows: zeros, by whole lines
+            const int c = n0 + (threadIdx.x & 31) * 8;
+            for (int r = m0 + threadIdx.x / 32; r < min(m0 + BM, g.M); r += 8)
+                if (c < g.N) *reinterpret_cast<u32x4*>(out + (size_t)r * g.N + c) = u32x4{0, 0, 0, 0};
+            return;
+        }
     } else {
         const int n_mt = *g.plan.mt_count;
         const int tiles = n_mt * g.n_nt;
