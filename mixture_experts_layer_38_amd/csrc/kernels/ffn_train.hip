@@ -26,6 +26,7 @@ hipError_t launch_ffn_train_tiles(int n, int E, int d, int F, const bf16* x, con
 hipError_t launch_decode_keep(int n_rows, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
                               const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act, bf16* h, hipStream_t s);
 
+size_t ffn_grad_ws_bytes(int n, int E, int d, int F);
 hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
                            const bf16* w3, const bf16* w2, const bf16* gate, const bf16* up, const bf16* dh, bf16* dx,
                            bf16* dw1, bf16* dw3, bf16* dw2, bf16* dgate, bf16* dup, bf16* act, void* ws,
@@ -182,10 +183,11 @@ hipError_t launch_ffn_train(int T, int K, int E, int d, int F, int dtype, const 
     return err;
 }
 
-// dgate, dup, act, then the row plan
+// dgate, dup, act, then the row plan (bf16: and what the weights' products need)
 size_t ffn_backward_ws_bytes(int T, int K, int E, int d, int F, int dtype) {
     const size_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
-    return 3 * align_up((size_t)T * K * F * es, 256) + row_plan_bytes(T * K, E);
+    return 3 * align_up((size_t)T * K * F * es, 256) +
+           (dtype == MOE_DTYPE_F32 ? row_plan_bytes(T * K, E) : ffn_grad_ws_bytes(T * K, E, d, F));
 }
 
 hipError_t launch_ffn_backward(int T, int K, int E, int d, int F, int dtype, const void* x, const int32_t* offsets,

@@ -51,13 +51,16 @@ struct TrainArgs {
     int M, N, K;  // TR_DW: results are [M][N]; else [rows][N], K the reduction of one product
     int lda, ldb;
     int n_mt, n_nt, sels;  // TR_DW: row tiles per result, results per expert
+    int parts;             // TR_DW: ranges of rows that are summed apart,
+    float* part;           // into [parts][E][sels][M][N] when there are several
     RowPlan plan;
     const int32_t* offsets;
 };
 
 // KT: K is not a multiple of the stage, so a [r][k] row's chunks past it are
 // masked (they would be the next row's; TR_DW has no such rows).
-template <int MODE, int BM, bool KT>
+// PART (TR_DW): fp32 sums of one range of rows.
+template <int MODE, int BM, bool KT, bool PART = false>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == 256 ? 1 : 2, BM == 256 ? 1 : 2)))
 void ffn_train_kernel(TrainArgs g) {
     constexpr bool WG = MODE == TR_DW;
@@ -81,9 +84,10 @@ void ffn_train_kernel(TrainArgs g) {
         // every XCD takes an eighth of each result's tiles: the experts' row
         // counts differ, the XCDs' shares of them do not
         const int per = (g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD;
-        const int res = slot / per;
+        const int res_part = slot / per;
         const int t = xcd * per + slot % per;
-        if (res >= g.E * g.sels || t >= g.n_mt * g.n_nt) return;
+        if (res_part >= g.E * g.sels * g.parts || t >= g.n_mt * g.n_nt) return;
+        const int res = res_part / g.parts;
         // Uniform values are put into scalar registers (the divisions ran in
         // vector ones), so that the descriptors made of them are scalar too.
         e = __builtin_amdgcn_readfirstlane(res / g.sels);
@@ -98,7 +102,13 @@ void ffn_train_kernel(TrainArgs g) {
         k_beg = __builtin_amdgcn_readfirstlane(min(max(g.offsets[e], 0), g.n_rows));
         k_len = max(__builtin_amdgcn_readfirstlane(min(g.offsets[e + 1], g.n_rows)) - k_beg, 0);
         out += (size_t)e * g.M * g.N;
-        if (k_len == 0) {  // an expert without rows: zeros, by whole lines
+        if constexpr (PART) {  // whole stages, but for the last range's end
+            const int p = __builtin_amdgcn_readfirstlane(res_part % g.parts);
+            const int beg = (int)((long long)k_len * p / g.parts) & ~63;
+            const int end = p + 1 < g.parts ? (int)((long long)k_len * (p + 1) / g.parts) & ~63 : k_len;
+            k_beg += beg;
+            k_len = end - beg;
+        } else if (k_len == 0) {  // an expert without rows: zeros, by whole lines
             const int c = n0 + (threadIdx.x & 31) * 8;
             for (int r = m0 + threadIdx.x / 32; r < min(m0 + BM, g.M); r += 8)
                 if (c < g.N) *reinterpret_cast<u32x4*>(out + (size_t)r * g.N + c) = u32x4{0, 0, 0, 0};
@@ -419,7 +429,33 @@ void ffn_train_kernel(TrainArgs g) {
                            : (wave == 0 ? sB0 : wave == 1 ? sB1 : wave == 2 ? sB2 : sA0);
     const int mrow = wm * (BM / 2), ncol = n0 + wn * 128;
     const int el = pf_lane_fresh();
-    if constexpr (MODE == TR_DACT) {
+    if constexpr (PART) {
+        // fp32 sums, 32 rows x 64 columns (8 KB) at a time
+        float* const sf = reinterpret_cast<float*>(st);
+        const int res_part = __builtin_amdgcn_readfirstlane(slot / ((g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD));
+        float* const dst = g.part + ((size_t)(res_part % g.parts) * g.E * g.sels + res_part / g.parts) * g.M * g.N;
+        const int lrow = el >> 4, lch = el & 15;
+#pragma unroll
+        for (int p = 0; p < 2 * NTB; ++p) {
+            const int mb = p >> 1, half = p & 1;
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int ch = nb * 8 + 2 * q + (el >> 5), rl = el & 31;
+                    const f32x16& a = acc[2 * half + nb][mb];
+                    *reinterpret_cast<f32x4*>(sf + rl * 64 + ((ch ^ (rl & 15)) << 2)) =
+                        f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+                }
+            const int c = ncol + half * 64 + lch * 4;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int rl = i * 4 + lrow, r = m0 + mrow + mb * 32 + rl;
+                const f32x4 v = *reinterpret_cast<const f32x4*>(sf + rl * 64 + ((lch ^ (rl & 15)) << 2));
+                if (r < g.M && c < g.N) *reinterpret_cast<f32x4*>(dst + (size_t)r * g.N + c) = v;
+            }
+        }
+    } else if constexpr (MODE == TR_DACT) {
         // fp32 sums, 32 rows x 64 columns (8 KB) at a time; then gate and up by whole lines
         float* const sf = reinterpret_cast<float*>(st);
         const int lrow = el >> 3, lch = el & 7;  // eight chunks of eight columns per row
@@ -539,9 +575,34 @@ hipError_t launch_tiles(const TrainArgs& g, int bm, unsigned grid, hipStream_t s
     return hipGetLastError();
 }
 
-// The result of P^T Q for every expert (and for a second P where a1 is given).
-hipError_t launch_dw(int n, int E, int M, int N, const bf16* p0, const bf16* p1, const bf16* q, bf16* out0,
-                         bf16* out1, const int32_t* offsets, hipStream_t s) {
+// Adds the ranges of rows in order; result blockIdx.y of E * sels.
+__global__ __launch_bounds__(256) void dw_reduce_kernel(size_t n, int parts, int sels, const float* __restrict__ part,
+                                                       bf16* __restrict__ out0, bf16* __restrict__ out1) {
+    const int res = blockIdx.y;
+    const float* src = part + (size_t)res * n;
+    bf16* dst = (res % sels ? out1 : out0) + (size_t)(res / sels) * n;
+    const size_t step = (size_t)gridDim.y * n;
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (size_t)gridDim.x * 1024) {
+        f32x4 v = *reinterpret_cast<const f32x4*>(src + i);
+        for (int p = 1; p < parts; ++p) v += *reinterpret_cast<const f32x4*>(src + p * step + i);
+        *reinterpret_cast<bf16x4*>(dst + i) = bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+    }
+}
+
+// Ranges that the rows of TR_DW are cut into: with few result tiles and long
+// groups, enough for two workgroups per compute unit, 512 rows or more each.
+int dw_ranges(int n, int E, int M, int N, int sels) {
+    const long tiles = (long)((M + 127) / 128) * ((N + TR_BN - 1) / TR_BN) * E * sels;
+    return (int)std::max(1L, std::min(512 / tiles, (long)n / E / 512));
+}
+size_t dw_part_bytes(int n, int E, int M, int N, int sels) {
+    const int parts = dw_ranges(n, E, M, N, sels);
+    return parts > 1 ? (size_t)parts * E * sels * M * N * sizeof(float) : 0;
+}
+
+// The result of P^T Q for every expert (and for a second P where p1 is given).
+hipError_t launch_dw(int n, int E, int M, int N, const bf16* p0, const bf16* p1, const bf16* q, bf16* out0, bf16* out1,
+                     const int32_t* offsets, float* part, hipStream_t s) {
     TrainArgs g{};
     g.a0 = p0;
     g.a1 = p1;
@@ -554,11 +615,21 @@ hipError_t launch_dw(int n, int E, int M, int N, const bf16* p0, const bf16* p1,
     g.N = g.ldb = N;
     g.sels = p1 != nullptr ? 2 : 1;
     g.offsets = offsets;
-    const int bm = n >= TR_DW_LONG * E ? 256 : 128;
+    g.parts = dw_ranges(n, E, M, N, g.sels);
+    g.part = part;
+    const int bm = g.parts == 1 && n >= TR_DW_LONG * E ? 256 : 128;
     g.n_mt = (M + bm - 1) / bm;
     g.n_nt = (N + TR_BN - 1) / TR_BN;
     const long per = ((long)g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD;
-    return launch_tiles<TR_DW, false>(g, bm, (unsigned)(per * E * g.sels * PF_XCD), s);
+    const unsigned grid = (unsigned)(per * E * g.sels * g.parts * PF_XCD);
+    if (g.parts == 1) return launch_tiles<TR_DW, false>(g, bm, grid, s);
+    ffn_train_kernel<TR_DW, 128, false, true><<<grid, 256, 0, s>>>(g);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const size_t each = (size_t)M * N;
+    dw_reduce_kernel<<<dim3((unsigned)std::min<size_t>((each + 1023) / 1024, 1024), E * g.sels), 256, 0, s>>>(
+        each, g.parts, g.sels, part, out0, out1);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -603,6 +674,11 @@ hipError_t launch_ffn_train_tiles(int n, int E, int d, int F, const bf16* x, con
     return launch_tiles<TR_DOWN, true>(g, bm, train_grid(n, E, bm, g.n_nt), s);
 }
 
+// The row plan, then the ranges' sums of one weight gradient after the other.
+size_t ffn_grad_ws_bytes(int n, int E, int d, int F) {
+    return row_plan_bytes(n, E) + std::max(dw_part_bytes(n, E, d, F, 1), dw_part_bytes(n, E, F, d, 2));
+}
+
 hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
                            const bf16* w3, const bf16* w2, const bf16* gate, const bf16* up, const bf16* dh, bf16* dx,
                            bf16* dw1, bf16* dw3, bf16* dw2, bf16* dgate, bf16* dup, bf16* act, void* ws,
@@ -611,6 +687,7 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
     RowPlan plan;
     hipError_t err = launch_row_plan(n, E, bm, offsets, ws, &plan, s);
     if (err != hipSuccess) return err;
+    float* part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + row_plan_bytes(n, E));
     auto grid = [&](int n_nt) { return train_grid(n, E, bm, n_nt); };
     TrainArgs g{};
     g.a0 = dh;
@@ -631,8 +708,8 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
                          : launch_tiles<TR_DACT, true>(g, bm, grid(g.n_nt), s);
     if (err != hipSuccess) return err;
     if (dw2 != nullptr) {
-        if ((err = launch_dw(n, E, d, F, dh, nullptr, act, dw2, nullptr, offsets, s)) != hipSuccess) return err;
-        if ((err = launch_dw(n, E, F, d, dgate, dup, x, dw1, dw3, offsets, s)) != hipSuccess) return err;
+        if ((err = launch_dw(n, E, d, F, dh, nullptr, act, dw2, nullptr, offsets, part, s)) != hipSuccess) return err;
+        if ((err = launch_dw(n, E, F, d, dgate, dup, x, dw1, dw3, offsets, part, s)) != hipSuccess) return err;
     }
     if (dx != nullptr) {
         g.a0 = dgate;

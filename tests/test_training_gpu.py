@@ -63,6 +63,8 @@ FFN_CASES = [
     (500, 2, 136, 1000, [129, 300, 0, 31, 255]),
     (90, 2, 128, 136, [0, 180]),
     (64, 2, 264, 200, [33, 31, 64, 0]),
+    (3000, 1, 136, 72, [3000]),  # few weight tiles, long groups: rows summed in ranges
+    (2200, 2, 64, 320, [2500, 1, 0]),
 ]
 
 
