@@ -20,6 +20,7 @@ size_t prefill_ws_bytes(int n_rows, int E, int d);
 hipError_t launch_ffn_prefill_keep(int n_rows, int E, int d, int F, const bf16* x, const int32_t* offsets,
                                    const bf16* w1, const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act,
                                    bf16* h, void* ws, hipStream_t s);
+size_t ffn_train_tiles_ws_bytes(int n, int E, int d, int F);
 hipError_t launch_ffn_train_tiles(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
                                   const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act, bf16* h, void* ws,
                                   hipStream_t s);
@@ -151,7 +152,8 @@ hipError_t backward_gemms(int n, int E, int d, int F, const float* x, const int3
 size_t ffn_train_ws_bytes(int T, int K, int E, int d, int F, int dtype) {
     const size_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
     return align_up((size_t)T * K * F * es, 256) +
-           (dtype == MOE_DTYPE_F32 ? row_plan_bytes(T * K, E) : std::max(row_plan_bytes(T * K, E), prefill_ws_bytes(T * K, E, d)));
+           (dtype == MOE_DTYPE_F32 ? row_plan_bytes(T * K, E)
+                                   : std::max(ffn_train_tiles_ws_bytes(T * K, E, d, F), prefill_ws_bytes(T * K, E, d)));
 }
 
 hipError_t launch_ffn_train(int T, int K, int E, int d, int F, int dtype, const void* x, const int32_t* offsets,

@@ -51,15 +51,18 @@ struct TrainArgs {
     int M, N, K;  // TR_DW: results are [M][N]; else [rows][N], K the reduction of one product
     int lda, ldb;
     int n_mt, n_nt, sels;  // TR_DW: row tiles per result, results per expert
-    int parts;             // TR_DW: ranges of rows that are summed apart,
-    float* part;           // into [parts][E][sels][M][N] when there are several
+    // Ranges of the reduction that are summed apart when there are several:
+    // TR_DW, of rows, into part [parts][E][sels][M][N]; TR_DX and TR_DOWN, of
+    // stages, into part [parts][rows][N].
+    int parts;
+    float* part;
     RowPlan plan;
     const int32_t* offsets;
 };
 
 // KT: K is not a multiple of the stage, so a [r][k] row's chunks past it are
 // masked (they would be the next row's; TR_DW has no such rows).
-// PART (TR_DW): fp32 sums of one range of rows.
+// PART: fp32 sums of one range of the reduction.
 template <int MODE, int BM, bool KT, bool PART = false>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == 256 ? 1 : 2, BM == 256 ? 1 : 2)))
 void ffn_train_kernel(TrainArgs g) {
@@ -78,8 +81,10 @@ void ffn_train_kernel(TrainArgs g) {
 
     const int xcd = blockIdx.x % PF_XCD, slot = blockIdx.x / PF_XCD;
     int e, row0 = 0, row_end = 0, m0 = 0, n0, k_beg = 0, k_len = g.K;
+    int range = 0;  // of g.parts
     const bf16 *A0 = g.a0, *A1 = g.a1, *B0 = g.b0, *B1 = g.b1;
     bf16* out = g.out0;
+    bool out_sel = false;  // TR_DW: the expert's second result
     if constexpr (WG) {
         // every XCD takes an eighth of each result's tiles: the experts' row
         // counts differ, the XCDs' shares of them do not
@@ -94,6 +99,7 @@ void ffn_train_kernel(TrainArgs g) {
         if (__builtin_amdgcn_readfirstlane(res % g.sels)) {
             A0 = g.a1;
             out = g.out1;
+            out_sel = true;
         }
         const int grp = t / (TR_GM * g.n_nt), gsize = min(TR_GM, g.n_mt - grp * TR_GM);
         const int rem = t - grp * TR_GM * g.n_nt;
@@ -103,9 +109,9 @@ void ffn_train_kernel(TrainArgs g) {
         k_len = max(__builtin_amdgcn_readfirstlane(min(g.offsets[e + 1], g.n_rows)) - k_beg, 0);
         out += (size_t)e * g.M * g.N;
         if constexpr (PART) {  // whole stages, but for the last range's end
-            const int p = __builtin_amdgcn_readfirstlane(res_part % g.parts);
-            const int beg = (int)((long long)k_len * p / g.parts) & ~63;
-            const int end = p + 1 < g.parts ? (int)((long long)k_len * (p + 1) / g.parts) & ~63 : k_len;
+            range = __builtin_amdgcn_readfirstlane(res_part % g.parts);
+            const int beg = (int)((long long)k_len * range / g.parts) & ~63;
+            const int end = range + 1 < g.parts ? (int)((long long)k_len * (range + 1) / g.parts) & ~63 : k_len;
             k_beg += beg;
             k_len = end - beg;
         } else if (k_len == 0) {  // an expert without rows: zeros, by whole lines
@@ -117,9 +123,13 @@ void ffn_train_kernel(TrainArgs g) {
     } else {
         const int n_mt = *g.plan.mt_count;
         const int tiles = n_mt * g.n_nt;
-        const int per = (tiles + PF_XCD - 1) / PF_XCD;
-        const int t = xcd * per + slot;
-        if (slot >= per || t >= tiles) return;
+        const int per = (tiles * (PART ? g.parts : 1) + PF_XCD - 1) / PF_XCD;
+        int t = xcd * per + slot;
+        if (slot >= per || t >= tiles * (PART ? g.parts : 1)) return;
+        if constexpr (PART) {
+            range = __builtin_amdgcn_readfirstlane(t % g.parts);
+            t /= g.parts;
+        }
         const PfTile tl = pf_tile(t, n_mt, g.n_nt, g.plan.mt_expert, g.plan.mt_row0, g.offsets, g.n_rows);
         e = tl.e;
         row0 = tl.row0;
@@ -130,7 +140,12 @@ void ffn_train_kernel(TrainArgs g) {
         if (MODE == TR_DX || MODE == TR_GATE) B1 += we;
     }
     const int nk1 = (k_len + TR_BK - 1) / TR_BK;  // stages of one product
-    const int nk = MODE == TR_DX ? 2 * nk1 : nk1;
+    const int nk_all = MODE == TR_DX ? 2 * nk1 : nk1;
+    // this workgroup's stages: all, or a range of them (TR_DW's ranges are in k_beg and k_len)
+    constexpr bool RANGE = PART && !WG;
+    const int ks = RANGE ? nk_all * range / g.parts : 0;
+    const int ke = RANGE ? nk_all * (range + 1) / g.parts : nk_all;
+    const int nk = ke - ks;
 
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
     const int lane = lane_id();
@@ -184,18 +199,18 @@ void ffn_train_kernel(TrainArgs g) {
         } else {
             const int seg = MODE == TR_DX && kt >= nk1;
             const int k0 = (kt - (seg ? nk1 : 0)) * TR_BK;
-            const int bytes = kt < nk ? ((row_end - row0) * g.lda - k0) * 2 : 0;
+            const int bytes = kt < ke ? ((row_end - row0) * g.lda - k0) * 2 : 0;
             return rsrc((seg ? A1 : A0) + (size_t)row0 * g.lda + k0, bytes);
         }
     };
     auto rs_b = [&](int kt, int which = 0) __attribute__((always_inline)) {
         if constexpr (BROWS) {
-            const int bytes = kt < nk ? (min(g.N - n0, MODE == TR_GATE ? 128 : TR_BN) * g.ldb - kt * TR_BK) * 2 : 0;
+            const int bytes = kt < ke ? (min(g.N - n0, MODE == TR_GATE ? 128 : TR_BN) * g.ldb - kt * TR_BK) * 2 : 0;
             return rsrc((which ? B1 : B0) + (size_t)n0 * g.ldb + kt * TR_BK, bytes);
         }
         const int seg = MODE == TR_DX && kt >= nk1;
         const int k0 = (kt - (seg ? nk1 : 0)) * TR_BK;
-        const int v = kt < nk ? min(k_len - k0, TR_BK) : 0;
+        const int v = kt < ke ? min(k_len - k0, TR_BK) : 0;
         return rsrc((seg ? B1 : B0) + (size_t)(k_beg + k0) * g.ldb + n0, v > 0 ? (v * g.ldb - n0) * 2 : 0);
     };
     auto ld_a = [&](__amdgpu_buffer_rsrc_t r, int kt, int j, bf16* dst) __attribute__((always_inline)) {
@@ -312,23 +327,23 @@ void ffn_train_kernel(TrainArgs g) {
     Frags fa, fb;
     auto step5 = [&](int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA) __attribute__((always_inline)) {
         // A(kt + 2) into pA early, B(kt + 2) into A(kt)'s unit after the barrier
-        const auto ra = rs_a(kt + 2);
-        const RsB rb = rs_bs(kt + 2);
+        const auto ra = rs_a(ks + kt + 2);
+        const RsB rb = rs_bs(ks + kt + 2);
         read(cA, cB, 1, fb);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) ld_a(ra, kt + 2, j, pA);
+        for (int j = 0; j < 3; ++j) ld_a(ra, ks + kt + 2, j, pA);
         mma(fa);
         weave(std::integral_constant<int, 3>{});
         __builtin_amdgcn_sched_barrier(0);
         read(cA, cB, 2, fa);
 #pragma unroll
-        for (int j = 3; j < 6; ++j) ld_a(ra, kt + 2, j, pA);
+        for (int j = 3; j < 6; ++j) ld_a(ra, ks + kt + 2, j, pA);
         mma(fb);
         weave(std::integral_constant<int, 3>{});
         __builtin_amdgcn_sched_barrier(0);
         read(cA, cB, 3, fb);
 #pragma unroll
-        for (int j = 6; j < NJA; ++j) ld_a(ra, kt + 2, j, pA);
+        for (int j = 6; j < NJA; ++j) ld_a(ra, ks + kt + 2, j, pA);
         mma(fa);
         weave(std::integral_constant<int, 2>{});
         __builtin_amdgcn_sched_barrier(0);
@@ -337,7 +352,7 @@ void ffn_train_kernel(TrainArgs g) {
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < NJB; ++j) ld_b(rb.r, kt + 2, j, cA);
+        for (int j = 0; j < NJB; ++j) ld_b(rb.r, ks + kt + 2, j, cA);
         read(nA, nB, 0, fa);
         mma(fb);
         weave(std::integral_constant<int, NJB>{});
@@ -347,13 +362,13 @@ void ffn_train_kernel(TrainArgs g) {
     // stage's two 16-wide parts.
     auto step3 = [&](int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA, bf16* pB) __attribute__((always_inline)) {
         constexpr int V = NLD / 2;
-        const auto ra = rs_a(kt + 2);
-        const RsB rb = rs_bs(kt + 2);
+        const auto ra = rs_a(ks + kt + 2);
+        const RsB rb = rs_bs(ks + kt + 2);
         auto lds = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = i0; i < i0 + V; ++i) {
-                if (i < NJA) ld_a(ra, kt + 2, i, pA);
-                else ld_b(rb.r, kt + 2, i - NJA, pB);
+                if (i < NJA) ld_a(ra, ks + kt + 2, i, pA);
+                else ld_b(rb.r, ks + kt + 2, i - NJA, pB);
             }
         };
         read(cA, cB, 1, fb);
@@ -372,12 +387,12 @@ void ffn_train_kernel(TrainArgs g) {
         __builtin_amdgcn_sched_barrier(0);
     };
     auto first = [&](int kt, bf16* dA, bf16* dB) __attribute__((always_inline)) {
-        const auto ra = rs_a(kt);
-        const RsB rb = rs_bs(kt);
+        const auto ra = rs_a(ks + kt);
+        const RsB rb = rs_bs(ks + kt);
 #pragma unroll
-        for (int j = 0; j < NJA; ++j) ld_a(ra, kt, j, dA);
+        for (int j = 0; j < NJA; ++j) ld_a(ra, ks + kt, j, dA);
 #pragma unroll
-        for (int j = 0; j < NJB; ++j) ld_b(rb.r, kt, j, dB);
+        for (int j = 0; j < NJB; ++j) ld_b(rb.r, ks + kt, j, dB);
     };
     if (nk > 0) {
         if constexpr (RING5) {
@@ -432,8 +447,10 @@ void ffn_train_kernel(TrainArgs g) {
     if constexpr (PART) {
         // fp32 sums, 32 rows x 64 columns (8 KB) at a time
         float* const sf = reinterpret_cast<float*>(st);
-        const int res_part = __builtin_amdgcn_readfirstlane(slot / ((g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD));
-        float* const dst = g.part + ((size_t)(res_part % g.parts) * g.E * g.sels + res_part / g.parts) * g.M * g.N;
+        // of the range: result e * sels + (which of them), or all rows
+        float* const dst = WG ? g.part + (((size_t)range * g.E + e) * g.sels + (out_sel ? 1 : 0)) * g.M * g.N
+                              : g.part + (size_t)range * g.n_rows * g.N;
+        const int r0 = WG ? m0 : row0, r_end = WG ? g.M : row_end;
         const int lrow = el >> 4, lch = el & 15;
 #pragma unroll
         for (int p = 0; p < 2 * NTB; ++p) {
@@ -450,9 +467,9 @@ void ffn_train_kernel(TrainArgs g) {
             const int c = ncol + half * 64 + lch * 4;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int rl = i * 4 + lrow, r = m0 + mrow + mb * 32 + rl;
+                const int rl = i * 4 + lrow, r = r0 + mrow + mb * 32 + rl;
                 const f32x4 v = *reinterpret_cast<const f32x4*>(sf + rl * 64 + ((lch ^ (rl & 15)) << 2));
-                if (r < g.M && c < g.N) *reinterpret_cast<f32x4*>(dst + (size_t)r * g.N + c) = v;
+                if (r < r_end && c < g.N) *reinterpret_cast<f32x4*>(dst + (size_t)r * g.N + c) = v;
             }
         }
     } else if constexpr (MODE == TR_DACT) {
@@ -589,6 +606,30 @@ __global__ __launch_bounds__(256) void dw_reduce_kernel(size_t n, int parts, int
     }
 }
 
+// TR_DX, TR_DOWN: adds the ranges of stages of the rows before *live (the groups' end).
+__global__ __launch_bounds__(256) void rows_reduce_kernel(int n_rows, int N, int parts, const float* __restrict__ part,
+                                                         const int32_t* __restrict__ live, bf16* __restrict__ out) {
+    const size_t n = (size_t)min(n_rows, *live) * N, step = (size_t)n_rows * N;
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (size_t)gridDim.x * 1024) {
+        f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
+        for (int p = 1; p < parts; ++p) v += *reinterpret_cast<const f32x4*>(part + p * step + i);
+        *reinterpret_cast<bf16x4*>(out + i) = bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+    }
+}
+
+// Ranges of the stages of a product of n rows and N columns over K: with few
+// tiles, enough for two workgroups per compute unit, eight stages or more each
+// (two experts of 24 rows, d 88, F 2944: the backward pass 94 -> 45 us).
+int row_ranges(int n, int E, int N, int K, int bm) {
+    if (bm != 128) return 1;
+    const long tiles = (long)row_plan_tiles(n, E, 128) * ((N + TR_BN - 1) / TR_BN);
+    return (int)std::max(1L, std::min(std::min(512 / tiles, (long)K / 256), 16L));
+}
+size_t row_part_bytes(int n, int E, int N, int K) {
+    const int parts = row_ranges(n, E, N, K, 128);
+    return parts > 1 ? (size_t)parts * n * N * sizeof(float) : 0;
+}
+
 // Ranges that the rows of TR_DW are cut into: with few result tiles and long
 // groups, enough for two workgroups per compute unit, 512 rows or more each.
 int dw_ranges(int n, int E, int M, int N, int sels) {
@@ -645,6 +686,28 @@ static unsigned train_grid(int n, int E, int bm, int n_nt) {
     return (unsigned)(((long)row_plan_tiles(n, E, bm) * n_nt + PF_XCD - 1) / PF_XCD * PF_XCD);
 }
 
+// A product over rows whose sum may be cut into ranges (K: of one product).
+template <int MODE>
+static hipError_t launch_rows(TrainArgs& g, int bm, int ranges, float* part, hipStream_t s) {
+    const unsigned grid = train_grid(g.n_rows, g.E, bm, g.n_nt * ranges);
+    if (ranges == 1) {
+        if constexpr (MODE == TR_DX)
+            if (g.K % 64 == 0) return launch_tiles<MODE, false>(g, bm, grid, s);
+        return launch_tiles<MODE, true>(g, bm, grid, s);
+    }
+    g.parts = ranges;
+    g.part = part;
+    ffn_train_kernel<MODE, 128, true, true><<<grid, 256, 0, s>>>(g);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const size_t vecs = (size_t)g.n_rows * g.N / 4;
+    rows_reduce_kernel<<<(unsigned)std::min<size_t>((vecs + 255) / 256, 2048), 256, 0, s>>>(
+        g.n_rows, g.N, ranges, part, g.offsets + g.E, g.out0);
+    return hipGetLastError();
+}
+
+size_t ffn_train_tiles_ws_bytes(int n, int E, int d, int F) { return row_plan_bytes(n, E) + row_part_bytes(n, E, d, F); }
+
 hipError_t launch_ffn_train_tiles(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
                                   const bf16* w3, const bf16* w2, bf16* gate, bf16* up, bf16* act, bf16* h, void* ws,
                                   hipStream_t s) {
@@ -671,12 +734,14 @@ hipError_t launch_ffn_train_tiles(int n, int E, int d, int F, const bf16* x, con
     g.N = d;
     g.K = g.lda = g.ldb = F;
     g.n_nt = (d + TR_BN - 1) / TR_BN;
-    return launch_tiles<TR_DOWN, true>(g, bm, train_grid(n, E, bm, g.n_nt), s);
+    return launch_rows<TR_DOWN>(g, bm, row_ranges(n, E, d, F, bm),
+                                reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + row_plan_bytes(n, E)), s);
 }
 
-// The row plan, then the ranges' sums of one weight gradient after the other.
+// The row plan, then the ranges' sums of one product after the other.
 size_t ffn_grad_ws_bytes(int n, int E, int d, int F) {
-    return row_plan_bytes(n, E) + std::max(dw_part_bytes(n, E, d, F, 1), dw_part_bytes(n, E, F, d, 2));
+    return row_plan_bytes(n, E) + std::max(std::max(dw_part_bytes(n, E, d, F, 1), dw_part_bytes(n, E, F, d, 2)),
+                                           row_part_bytes(n, E, d, 2 * F));
 }
 
 hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
@@ -720,8 +785,7 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
         g.N = g.ldb = d;
         g.K = g.lda = F;
         g.n_nt = (d + TR_BN - 1) / TR_BN;
-        err = F % 64 == 0 ? launch_tiles<TR_DX, false>(g, bm, grid(g.n_nt), s)
-                             : launch_tiles<TR_DX, true>(g, bm, grid(g.n_nt), s);
+        err = launch_rows<TR_DX>(g, bm, row_ranges(n, E, d, 2 * F, bm), part, s);
     }
     return err;
 }

@@ -297,7 +297,8 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
 constexpr int RW_T = 128, RW_K = 64, RW_H = RW_K / 16;
 template <bool VEC>
 __global__ __launch_bounds__(256) void route_dw_kernel(int T, int d, int E, const bf16* __restrict__ x,
-                                                      const float* __restrict__ dl, float* __restrict__ part) {
+                                                      const float* __restrict__ dl, float* __restrict__ part,
+                                                      bf16* __restrict__ out) {
     __shared__ __align__(16) bf16 sX[RW_K * RW_T], sH[RW_K * RW_T], sL[RW_K * RW_T];
     const int e0 = blockIdx.x * RW_T, c0 = blockIdx.y * RW_T;
     const int t_beg = (int)((long long)T * blockIdx.z / gridDim.z);
@@ -381,7 +382,14 @@ __global__ __launch_bounds__(256) void route_dw_kernel(int T, int d, int E, cons
                 const int e = e0 + wn * 64 + nb * 32 + 8 * q + 4 * fhalf;
                 const f32x16& a = acc[nb][mb];
                 const f32x4 v[2] = {f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]}, f32x4{}};
-                if (e < E) epi(blockIdx.z, 0, c, e, E, v);
+                if (e >= E) continue;
+                if (gridDim.z > 1) {
+                    epi(blockIdx.z, 0, c, e, E, v);
+                } else {  // one part: the result itself
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (e + j < E) out[(size_t)c * E + e + j] = (bf16)v[0][j];
+                }
             }
     }
 }
@@ -425,7 +433,7 @@ hipError_t route_products(int n_tok, int d, int E, int K, const float* x, const 
         err = with_tile(E <= 64 ? 64 : gm_tile((long)tiles(E, 128) * tiles(d, 128) * parts), [&](auto t) {
             constexpr int T = decltype(t)::value;
             gemm_f32_kernel<T, GM_TN, false, 1, true, VEC><<<dim3(tiles(E, T), tiles(d, T), parts), 256, 0, s>>>(
-                g, EpiPart{part, d});
+                g, EpiPart{parts > 1 ? part : dwr, d});
             return hipGetLastError();
         });
         if (err != hipSuccess) return err;
@@ -444,8 +452,8 @@ hipError_t route_products(int n_tok, int d, int E, int K, const bf16* x, const b
         if ((err = hipGetLastError()) != hipSuccess) return err;
     }
     if (dwr != nullptr) {
-        route_dw_kernel<VEC><<<dim3((E + RW_T - 1) / RW_T, (d + RW_T - 1) / RW_T, parts), 256, 0, s>>>(n_tok, d, E, x, dl,
-                                                                                                       part);
+        route_dw_kernel<VEC><<<dim3((E + RW_T - 1) / RW_T, (d + RW_T - 1) / RW_T, parts), 256, 0, s>>>(
+            n_tok, d, E, x, dl, part, dwr);
         if ((err = hipGetLastError()) != hipSuccess) return err;
     }
     return hipSuccess;
@@ -460,7 +468,7 @@ hipError_t route_gradients(int n_tok, int d, int E, int K, const void* x, const 
                                                     assign_row, dl, (T*)dx, (T*)dwr, part, parts, s);
     };
     const hipError_t err = E % 8 == 0 ? run(std::true_type{}) : run(std::false_type{});
-    if (err != hipSuccess || dwr == nullptr) return err;
+    if (err != hipSuccess || dwr == nullptr || parts == 1) return err;
     const size_t n = (size_t)d * E;
     route_dw_reduce_kernel<T><<<(unsigned)std::min<size_t>((n + 1023) / 1024, 4096), 256, 0, s>>>(n, parts, part, (T*)dwr);
     return hipGetLastError();
