@@ -325,37 +325,50 @@ void ffn_train_kernel(TrainArgs g) {
     // After the third: this wave's reads of the stage are done and its loads of
     // stage kt + 1 have landed; the barrier then frees the stage's units.
     Frags fa, fb;
-    auto step5 = [&](int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA) __attribute__((always_inline)) {
-        // A(kt + 2) into pA early, B(kt + 2) into A(kt)'s unit after the barrier
+    // Five-unit ring: the early operand of stage kt is in unit 2 kt % 5, the late
+    // one in the next; early(kt + 2) goes into unit p during the first three
+    // quarters, late(kt + 2) into early(kt)'s unit after the barrier.  The early
+    // operand is the weights, which stream from HBM (TR_DW: the m side).
+    constexpr bool SW = !WG;
+    auto step5 = [&](int kt, bf16* c1, bf16* c2, const bf16* n1, const bf16* n2, bf16* p) __attribute__((always_inline)) {
+        const bf16 *cA = SW ? c2 : c1, *cB = SW ? c1 : c2, *nA = SW ? n2 : n1, *nB = SW ? n1 : n2;
         const auto ra = rs_a(ks + kt + 2);
         const RsB rb = rs_bs(ks + kt + 2);
+        auto early = [&](int j) __attribute__((always_inline)) {
+            if constexpr (SW) ld_b(rb.r, ks + kt + 2, j, p);
+            else ld_a(ra, ks + kt + 2, j, p);
+        };
+        static_assert(!RING5 || (NJA == 8 && NJB == 8), "loads of a half");
         read(cA, cB, 1, fb);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) ld_a(ra, ks + kt + 2, j, pA);
+        for (int j = 0; j < 3; ++j) early(j);
         mma(fa);
         weave(std::integral_constant<int, 3>{});
         __builtin_amdgcn_sched_barrier(0);
         read(cA, cB, 2, fa);
 #pragma unroll
-        for (int j = 3; j < 6; ++j) ld_a(ra, ks + kt + 2, j, pA);
+        for (int j = 3; j < 6; ++j) early(j);
         mma(fb);
         weave(std::integral_constant<int, 3>{});
         __builtin_amdgcn_sched_barrier(0);
         read(cA, cB, 3, fb);
 #pragma unroll
-        for (int j = 6; j < NJA; ++j) ld_a(ra, ks + kt + 2, j, pA);
+        for (int j = 6; j < 8; ++j) early(j);
         mma(fa);
         weave(std::integral_constant<int, 2>{});
         __builtin_amdgcn_sched_barrier(0);
         PF_WAIT_LGKM0();
-        PF_WAIT_VM(NJA);
+        PF_WAIT_VM(8);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < NJB; ++j) ld_b(rb.r, ks + kt + 2, j, cA);
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (SW) ld_a(ra, ks + kt + 2, j, c1);
+            else ld_b(rb.r, ks + kt + 2, j, c1);
+        }
         read(nA, nB, 0, fa);
         mma(fb);
-        weave(std::integral_constant<int, NJB>{});
+        weave(std::integral_constant<int, 8>{});
         __builtin_amdgcn_sched_barrier(0);
     };
     // Stage kt + 2 into slot (kt + 2) % 3, half of its loads in each of the
@@ -397,11 +410,11 @@ void ffn_train_kernel(TrainArgs g) {
     if (nk > 0) {
         if constexpr (RING5) {
             bf16 *const u0 = sA0, *const u1 = sB0, *const u2 = sA1, *const u3 = sB1, *const u4 = sU4;
-            first(0, u0, u1);
-            first(1, u2, u3);
+            first(0, SW ? u1 : u0, SW ? u0 : u1);
+            first(1, SW ? u3 : u2, SW ? u2 : u3);
             PF_WAIT_VM(NLD);
             __builtin_amdgcn_s_barrier();
-            read(u0, u1, 0, fa);
+            read(SW ? u1 : u0, SW ? u0 : u1, 0, fa);
             const int main = nk - nk % 5;
             for (int k = 0; k < main; k += 5) {
                 step5(k, u0, u1, u2, u3, u4);
