@@ -201,6 +201,7 @@ __device__ __forceinline__ bf16x8 load_weights(const bf16* row, int e, int E) {
 // straight from cache; the products then lie in the LDS as fp32 rows (chunks
 // swizzled by row), to which each wave adds the tokens' grouped rows, whole
 // lines at a time.  Bound by those rows (T K d elements).
+constexpr int RX_K = 8;  // grouped rows of a token whose loads go out together
 constexpr int RX_T = 64, RX_C = 128, RX_E = 64, RX_LD = RX_E + 8;
 template <bool VEC>
 __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int K, const float* __restrict__ dl,
@@ -237,8 +238,37 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
 #pragma unroll
         for (int h = 0; h < 2; ++h) load_scores<VEC>(v[h], drow, e0 + lc + 8 * h, E, on);
     };
-    load(0);
-    for (int e0 = 0; e0 < E; e0 += RX_E) {
+    // the wave's 16 tokens, four at a time; the lane's eight columns
+    const int c = c0 + (lane & 15) * 8, cc = min(c, d - 8);
+    const int n = T * K;
+    u32x4 raw[RX_K];
+    uint32_t own = 0;  // which of raw are the token's
+    auto fetch = [&](int i) {
+        const int32_t* slots = sRow + (wave * (RX_T / 4) + 4 * i + (lane >> 4)) * K;
+        own = 0;
+#pragma unroll
+        for (int k = 0; k < RX_K; ++k) {
+            const int r = k < K ? slots[k] : -1;
+            const bool in = (unsigned)r < (unsigned)n;
+            own |= in ? 1u << k : 0u;
+            raw[k] = load16(rows + (size_t)(in ? r : 0) * d + cc);  // (row 0 is never added then)
+        }
+    };
+    float sum[RX_T / 16][8];
+    auto add = [&](int i, float (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < RX_K; ++k) {
+            const bf16x8 x = as_bf16x8(raw[k]);
+            if (own >> k & 1)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += (float)x[j];
+        }
+        if (K > RX_K)
+            add_rows(v, rows, sRow + (wave * (RX_T / 4) + 4 * i + (lane >> 4)) * K + RX_K, K - RX_K, n, d, cc);
+    };
+    auto chunk = [&](int e0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             bf16x8 hi, lo;
@@ -262,7 +292,19 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
                     acc[tb] = mfma32(cw[ks], lo, acc[tb]);
                 }
         __syncthreads();
+    };
+    load(0);
+    if (rows != nullptr) {
+        __syncthreads();  // sRow
+        // a chunk of experts under each fetch's latency
+#pragma unroll
+        for (int i = 0; i < RX_T / 16; ++i) {
+            fetch(i);
+            if (i * RX_E < E) chunk(i * RX_E);
+            add(i, sum[i]);
+        }
     }
+    for (int e0 = rows != nullptr ? RX_T / 16 * RX_E : 0; e0 < E; e0 += RX_E) chunk(e0);
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
@@ -272,19 +314,18 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
                 f32x4{acc[tb][4 * q], acc[tb][4 * q + 1], acc[tb][4 * q + 2], acc[tb][4 * q + 3]};
         }
     __syncthreads();
-    const int ch = 2 * (lane & 15), c = c0 + (lane & 15) * 8;
+    const int ch = 2 * (lane & 15);
     if (c >= d) return;
-#pragma unroll 2
+#pragma unroll
     for (int i = 0; i < RX_T / 16; ++i) {
         const int tl = wave * (RX_T / 4) + 4 * i + (lane >> 4), t = t0 + tl;
         if (t >= T) break;
         const f32x4 a = *reinterpret_cast<const f32x4*>(sP + tl * RX_C + ((ch ^ (tl & 31)) << 2));
         const f32x4 b = *reinterpret_cast<const f32x4*>(sP + tl * RX_C + (((ch + 1) ^ (tl & 31)) << 2));
-        float sum[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        if (rows != nullptr) add_rows(sum, rows, sRow + tl * K, K, T * K, d, c);
+        const float p[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
         bf16x8 o;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = (bf16)sum[j];
+        for (int j = 0; j < 8; ++j) o[j] = (bf16)(rows != nullptr ? sum[i][j] + p[j] : p[j]);
         *reinterpret_cast<bf16x8*>(dx + (size_t)t * d + c) = o;
     }
 }
