@@ -241,17 +241,17 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
     // the wave's 16 tokens, four at a time; the lane's eight columns
     const int c = c0 + (lane & 15) * 8, cc = min(c, d - 8);
     const int n = T * K;
-    u32x4 raw[RX_K];
-    uint32_t own = 0;  // which of raw are the token's
+    u32x4 raw[2][RX_K];
+    uint32_t own[2];  // which of raw are the token's
     auto fetch = [&](int i) {
         const int32_t* slots = sRow + (wave * (RX_T / 4) + 4 * i + (lane >> 4)) * K;
-        own = 0;
+        own[i & 1] = 0;
 #pragma unroll
         for (int k = 0; k < RX_K; ++k) {
             const int r = k < K ? slots[k] : -1;
             const bool in = (unsigned)r < (unsigned)n;
-            own |= in ? 1u << k : 0u;
-            raw[k] = load16(rows + (size_t)(in ? r : 0) * d + cc);  // (row 0 is never added then)
+            own[i & 1] |= in ? 1u << k : 0u;
+            raw[i & 1][k] = load16(rows + (size_t)(in ? r : 0) * d + cc);  // (row 0 is never added then)
         }
     };
     float sum[RX_T / 16][8];
@@ -260,8 +260,8 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
 #pragma unroll
         for (int k = 0; k < RX_K; ++k) {
-            const bf16x8 x = as_bf16x8(raw[k]);
-            if (own >> k & 1)
+            const bf16x8 x = as_bf16x8(raw[i & 1][k]);
+            if (own[i & 1] >> k & 1)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] += (float)x[j];
         }
@@ -296,10 +296,11 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
     load(0);
     if (rows != nullptr) {
         __syncthreads();  // sRow
-        // a chunk of experts under each fetch's latency
+        // the next fetch and a chunk of experts under each fetch's latency
+        fetch(0);
 #pragma unroll
         for (int i = 0; i < RX_T / 16; ++i) {
-            fetch(i);
+            if (i + 1 < RX_T / 16) fetch(i + 1);
             if (i * RX_E < E) chunk(i * RX_E);
             add(i, sum[i]);
         }
