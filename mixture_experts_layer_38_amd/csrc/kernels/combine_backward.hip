@@ -1,7 +1,8 @@
 // Backward pass of the weighted combine y[t] = sum_k w[t,k] h[row(t,k)]:
 //   dh[row(t,k)] = w[t,k] dy[t],   dw[t,k] = <dy[t], h[row(t,k)]>
 // Bound by memory: h is read and dh written once (2 T K d elements), dy is
-// read once from HBM and K times from cache.
+// read once from HBM and K times from cache.  4096 tokens, eight slots, d 7168:
+// 204 us for 1.0 GB, 4.9 TB/s, what a large copy reaches.
 #include <algorithm>
 
 #include "../device_common.h"

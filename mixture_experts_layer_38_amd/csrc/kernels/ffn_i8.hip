@@ -3,7 +3,15 @@
 //   g = (sum_k a_q w1_q) s_a s1,  u likewise,  act = bf16(silu(g) u),
 //   h = (sum_f act_q w2_q) s_act s2
 // The integer sums are exact in 32 bits (at most 65536 * 127 * 127 < 2^31),
-// so their order does not matter; scales and the gate are fp32.
+// so their order does not matter; scales and the gate are fp32.  act is rounded
+// to bf16 before its quantisation because it is an output of the call; that
+// rounding (at most 2^-9 of the value) is no larger than the half step, 1 / 254
+// of the row's maximum, that the quantisation rounds by.
+//
+// Decode batches stream the weights (ffn_decode.hip), larger ones use the tiled
+// GEMMs (ffn_prefill.hip), whose stages then hold twice the values: Mixtral
+// shape, 32 tokens 261 us (bf16 weights: 483), 8192 tokens 2.68 ms, 2150 TOP/s
+// over the whole call (bf16: 4.75 ms).
 #include "../device_common.h"
 #include "../launch.h"
 #include "ffn_tiles.h"

@@ -33,6 +33,11 @@
 // LDS reads of each 16-wide k quarter are interleaved with the MFMAs of the
 // quarter before.  Other K use a generic variant further down.
 //
+// Variants.  The training pass stores the gate and up sums beside act; 8-bit
+// rows and weights go through the same stages two values to a bf16's place, into
+// int32 accumulators (16384 rows, 8 experts, d 4096, F 14336: gate/up 1.77 ms,
+// 2.2 POP/s, against 3.1 ms in bf16).
+//
 // Order.  Workgroup b runs on XCD b % 8.  The tiles are listed expert by
 // expert in groups of at most PF_GM row tiles of one expert (row tile fastest
 // inside a group), and XCD x takes the x-th contiguous eighth of that list, so

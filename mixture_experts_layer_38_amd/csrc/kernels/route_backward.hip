@@ -7,6 +7,10 @@
 //   dl[t, e] += d_aux E / T p_e (f_e - sum_j f_j p_j) + d_z 2 / T lse_t softmax(l_t)_e
 // Then dx[t] = sum_k dx_perm[row(t,k)] + sum_e dl[t,e] W_r[:,e] and
 // dW_r = x^T dl.  dl stays fp32 throughout.
+//
+// Bound by memory where tokens are many: 4096 tokens, 256 experts, eight slots,
+// d 7168 in bf16 take 206 us: scores 10, dx 133 (0.59 GB, 4.4 TB/s), dW_r 59 and
+// the sum of its four parts 6.
 #include <algorithm>
 #include <type_traits>
 
@@ -200,7 +204,8 @@ __device__ __forceinline__ bf16x8 load_weights(const bf16* row, int e, int E) {
 // through the LDS (64 experts at a time, split), the router weights come
 // straight from cache; the products then lie in the LDS as fp32 rows (chunks
 // swizzled by row), to which each wave adds the tokens' grouped rows, whole
-// lines at a time.  Bound by those rows (T K d elements).
+// lines at a time.  Bound by those rows (T K d elements); their loads are in
+// flight while the products run (after them: 183 us instead of 133).
 constexpr int RX_K = 8;  // grouped rows of a token whose loads go out together
 constexpr int RX_T = 64, RX_C = 128, RX_E = 64, RX_LD = RX_E + 8;
 template <bool VEC>
