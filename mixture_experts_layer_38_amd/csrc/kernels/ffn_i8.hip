@@ -5,7 +5,7 @@
 // The integer sums are exact in 32 bits (at most 65536 * 127 * 127 < 2^31),
 // so their order does not matter; scales and the gate are fp32.  act is rounded
 // to bf16 before its quantisation because it is an output of the call; that
-// rounding (at most 2^-9 of the value) is no larger than the half step, 1 / 254
+// rounding (at most 2^-8 of the value) is no larger than the half step, 1 / 254
 // of the row's maximum, that the quantisation rounds by.
 //
 // Decode batches stream the weights (ffn_decode.hip), larger ones use the tiled

@@ -173,8 +173,9 @@ __global__ __launch_bounds__(256) void route_add_rows_kernel(int T, int K, int d
 
 // ---- bf16: products on the bf16 MFMAs ------------------------------------------
 // An fp32 score gradient enters as two bf16 values, hi = bf16(v) and lo =
-// bf16(v - hi), so the product with exact bf16 factors is off by at most 2^-18
-// of its terms, below what the sums' fp32 additions lose.
+// bf16(v - hi), each rounding at most 2^-8 of what it rounds, so the product with
+// exact bf16 factors is off by at most 2^-16 of its terms, a 256th of the result's
+// own rounding.
 __device__ __forceinline__ void split8(const float (&v)[8], bf16x8& hi, bf16x8& lo) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

@@ -21,10 +21,11 @@ DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 SLACK = 64
 
 
-def assert_close(name, got, ref, size, K, dtype, inner=0, floor=1e-37):
+def assert_close(name, got, ref, size, K, dtype, inner=0, floor=1e-37, split=0.0):
     """got against the 64-bit ref; inner: roundings of the factors on the way (of `dtype`);
-    floor: what is lost to fp32's smallest numbers."""
-    u, v = U[dtype], 2.0 ** -24 * (K + SLACK)
+    floor: what is lost to fp32's smallest numbers; split: what a factor held as two bf16
+    values is off by (2^-8 of the residual, itself 2^-8 of the value)."""
+    u, v = U[dtype], 2.0 ** -24 * (K + SLACK) + split
     got, diff = got.double(), (got.double() - ref).abs()
     assert torch.isfinite(got).all(), f"{name}: non-finite values"
     bound = (inner * u + v) * size + u * ref.abs() + floor

@@ -167,6 +167,30 @@ def test_forward_i8_replays_in_a_graph():
             torch.cuda.synchronize()
 
 
+def test_i8_rows_past_32_bit_offsets():
+    """Activations of more than 2^31 values: the last rows."""
+    n, d, F, E = 40000, 128, 57344, 1
+    g = _gen(41)
+    assert n * F > 2 ** 31
+    x = torch.randn((n, d), generator=g, device="cuda").to(torch.bfloat16)
+    (w1, s1), (w3, s3), (w2, s2) = _weights(g, E, F, d), _weights(g, E, F, d), _weights(g, E, d, F)
+    p = moe.problem(n, d, E, 1, F, "bf16")
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    act = torch.empty((n, F), dtype=torch.bfloat16, device="cuda")
+    h = torch.empty_like(x)
+    ws = torch.empty(moe.moe_expert_ffn_i8_workspace_size(p), dtype=torch.uint8, device="cuda")
+    moe.moe_expert_ffn_i8(p, x, off, moe.i8_weights(w1, s1, w3, s3, w2, s2), act, h, ws)
+    torch.cuda.synchronize()
+    xq, xs = plain64.quantize(x[-64:])
+    ag = (xq @ w1[0].double().T) * xs.double() * s1[0].double()
+    ref = ag * torch.sigmoid(ag) * ((xq @ w3[0].double().T) * xs.double() * s3[0].double())
+    unit = (32 + 2 * ag.abs()) * 2.0 ** -24  # as in test_ffn_i8
+    assert ((act[-64:].double() - ref).abs() <= (2.0 ** -8 + unit) * ref.abs() + 1e-37).all()
+    hq, hs = plain64.quantize(act[-64:])
+    ref = (hq @ w2[0].double().T) * hs.double() * s2[0].double()
+    assert ((h[-64:].double() - ref).abs() <= (2.0 ** -8 + 8 * 2.0 ** -24) * ref.abs() + 1e-37).all()
+
+
 def test_fp32_layer_has_no_8_bit_form():
     z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
     layer = MoELayer(4, 64, 2, 1, 64, "f32", z(64, 2), z(2, 64, 64), z(2, 64, 64), z(2, 64, 64))
