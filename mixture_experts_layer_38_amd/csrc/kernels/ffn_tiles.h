@@ -88,6 +88,69 @@ int prefill_max_mtiles(int n_rows, int E);
 struct RowPlan {
     const int32_t *mt_count = nullptr, *mt_expert = nullptr, *mt_row0 = nullptr;
 };
+// The row tiles of the groups as a wave sees them: from a plan, or, for up to
+// 64 experts, found by the wave itself from the group offsets (lane e holds
+// expert e), which saves a launch and the chain of loads through the plan.  The
+// order is the plan's: an expert's tiles in groups of at most PF_GM, of balanced
+// sizes, the groups of one expert after another.
+struct GroupTiles {
+    static constexpr int kMax = kWave;
+    RowPlan plan;
+    const int32_t* offsets;
+    int bm, count;
+    int beg = 0, nt = 0, incl = 0;  // lane e: first row, tiles, tiles up to and with expert e
+    __device__ GroupTiles(const RowPlan& p, int E, int bm_, const int32_t* offs) : plan(p), offsets(offs), bm(bm_) {
+        if (plan.mt_count != nullptr) {
+            count = *plan.mt_count;
+            return;
+        }
+        const int e = lane_id();
+        beg = e < E ? offs[e] : 0;
+        nt = e < E ? (max(offs[e + 1] - beg, 0) + bm - 1) / bm : 0;
+        incl = nt;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int v = __shfl_up(incl, o);
+            if (e >= o) incl += v;
+        }
+        count = __builtin_amdgcn_readlane(incl, kWave - 1);
+    }
+    // Row tile m (< count) of the list: expert, its tiles before m and all of them.
+    __device__ void find(int m, int& e, int& j, int& n) const {
+        e = __popcll(__ballot(incl <= m));
+        n = __builtin_amdgcn_readlane(nt, e);
+        j = m - (__builtin_amdgcn_readlane(incl, e) - n);
+    }
+    // The same tile's expert and first row.
+    __device__ void rows(int m, int& e, int& row0) const {
+        if (plan.mt_count != nullptr) {
+            e = plan.mt_expert[m] & 0x7FF;
+            row0 = plan.mt_row0[m];
+            return;
+        }
+        int j, n;
+        find(m, e, j, n);
+        row0 = __builtin_amdgcn_readlane(beg, e) + j * bm;
+    }
+    __device__ PfTile tile(int t, int n_nt, int n_rows) const {
+        if (plan.mt_count != nullptr) return pf_tile(t, count, n_nt, plan.mt_expert, plan.mt_row0, offsets, n_rows);
+        PfTile r;
+        const int m = __builtin_amdgcn_readfirstlane(t / n_nt);
+        int j, n;
+        find(m, r.e, j, n);
+        const int ng = (n + PF_GM - 1) / PF_GM, base = n / ng, extra = n % ng;
+        const int big = extra * (base + 1);  // group g: base + (g < extra) tiles
+        const int g = j < big ? j / (base + 1) : extra + (j - big) / base;
+        const int gsize = base + (g < extra ? 1 : 0), first = g * base + min(g, extra);
+        const int rem = t - (m - j + first) * n_nt;
+        r.mt = m - j + first + rem % gsize;
+        r.nt = rem / gsize;
+        r.row0 = __builtin_amdgcn_readlane(beg, r.e) + (first + rem % gsize) * bm;
+        r.row_end = min(offsets[r.e + 1], n_rows);
+        return r;
+    }
+};
+
 // What a variant of the expert-GEMM kernels takes beyond the layer's forward
 // pass:
 // PfKeep (gate/up GEMM of the training pass): both projections are stored too,

@@ -120,7 +120,7 @@ hipError_t weight_product(const GemmArgs<float, float>& g, int sels, EpiWeights<
     });
 }
 
-// tile: the plan's row tiles, which are the products' tiles too.
+// tile: rows of the row tiles, which are the products' tiles too.
 hipError_t train_gemms(int n, int E, int d, int F, const float* x, const int32_t* offsets, const float* w1,
                        const float* w3, const float* w2, float* gate, float* up, float* act, float* h, int tile,
                        const RowPlan& plan, hipStream_t s) {
@@ -176,7 +176,7 @@ hipError_t launch_ffn_train(int T, int K, int E, int d, int F, int dtype, const 
     if (dtype == MOE_DTYPE_F32) {
         RowPlan plan;
         const int tile = rows_tile(n, E, std::min(d, F));
-        if ((err = launch_row_plan(n, E, tile, offsets, rest, &plan, s)) != hipSuccess) return err;
+        if (E > GroupTiles::kMax && (err = launch_row_plan(n, E, tile, offsets, rest, &plan, s)) != hipSuccess) return err;
         err = train_gemms(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3, (const float*)w2,
                           (float*)gate, (float*)up, (float*)base, (float*)h, tile, plan, s);
     } else if (T <= 64) {  // the forward pass's choice: few rows per expert, bound by the weights
@@ -213,7 +213,7 @@ hipError_t launch_ffn_backward(int T, int K, int E, int d, int F, int dtype, con
     if (dtype == MOE_DTYPE_F32) {
         RowPlan plan;
         const int tile = rows_tile(n, E, std::min(d, F));
-        if ((err = launch_row_plan(n, E, tile, offsets, rest, &plan, s)) != hipSuccess) return err;
+        if (E > GroupTiles::kMax && (err = launch_row_plan(n, E, tile, offsets, rest, &plan, s)) != hipSuccess) return err;
         err = backward_gemms(n, E, d, F, (const float*)x, offsets, (const float*)w1, (const float*)w3,
                              (const float*)w2, (const float*)gate, (const float*)up, (const float*)dh, (float*)dx,
                              (float*)dw1, (float*)dw3, (float*)dw2, (float*)dgate, (float*)dup, (float*)act, tile, plan,

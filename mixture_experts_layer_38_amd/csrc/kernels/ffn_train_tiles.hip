@@ -55,20 +55,21 @@ constexpr int TR_DW_LONG = 512;
 constexpr int TR_GM = 8;  // row tiles per group in TR_DW's order
 
 struct TrainArgs {
-    const bf16 *a0, *a1;  // rows (TR_DX: of both products; TR_DW: the m side of both results)
-    const bf16 *b0, *b1;  // the n side (TR_GATE: both weights)
+    const bf16 *a0, *a1, *a2;  // rows (TR_DX: of both products; TR_DW: the m sides of its three results)
+    const bf16 *b0, *b1, *b2;  // the n side (TR_GATE: both weights; TR_DW: of the three results)
     bf16 *out0, *out1, *out2;
     const bf16 *gate, *up;
     int n_rows, E;
-    int M, N, K;  // TR_DW: results are [M][N]; else [rows][N], K the reduction of one product
-    int lda, ldb;
-    int n_mt, n_nt, sels;  // TR_DW: row tiles per result, results per expert
+    // [rows][N], K the reduction of one product; TR_DW: an expert's first result
+    // is [M][N], the other two [N][M]
+    int M, N, K;
+    int lda, ldb, n_nt;
     // Ranges of the reduction that are summed apart when there are several:
-    // TR_DW, of rows, into part [parts][E][sels][M][N]; TR_DX and TR_DOWN, of
+    // TR_DW, of rows, into part [parts][E][3][M N]; TR_DX and TR_DOWN, of
     // stages, into part [parts][rows][N].
     int parts;
     float* part;
-    RowPlan plan;
+    RowPlan plan;  // mt_count NULL: up to 64 experts, whose row tiles each workgroup finds itself
     const int32_t* offsets;
 };
 
@@ -96,57 +97,69 @@ void ffn_train_kernel(TrainArgs g) {
     int range = 0;  // of g.parts
     const bf16 *A0 = g.a0, *A1 = g.a1, *B0 = g.b0, *B1 = g.b1;
     bf16* out = g.out0;
-    bool out_sel = false;  // TR_DW: the expert's second result
+    int M = g.M, N = g.N, lda = g.lda, ldb = g.ldb;
+    int sel = 0;  // TR_DW: which of the expert's results
+    // Uniform values are put into scalar registers (divisions and lane reads run
+    // in vector ones), so that the descriptors made of them are scalar too.
+    const auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     if constexpr (WG) {
         // every XCD takes an eighth of each result's tiles: the experts' row
         // counts differ, the XCDs' shares of them do not
-        const int per = (g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD;
-        const int res_part = slot / per;
-        const int t = xcd * per + slot % per;
-        if (res_part >= g.E * g.sels * g.parts || t >= g.n_mt * g.n_nt) return;
-        const int res = res_part / g.parts;
-        // Uniform values are put into scalar registers (the divisions ran in
-        // vector ones), so that the descriptors made of them are scalar too.
-        e = __builtin_amdgcn_readfirstlane(res / g.sels);
-        if (__builtin_amdgcn_readfirstlane(res % g.sels)) {
-            A0 = g.a1;
-            out = g.out1;
-            out_sel = true;
+        const auto tiles_of = [](int m, int n) { return ((m + BM - 1) / BM) * ((n + TR_BN - 1) / TR_BN); };
+        const int per0 = (tiles_of(M, N) + PF_XCD - 1) / PF_XCD, per1 = (tiles_of(N, M) + PF_XCD - 1) / PF_XCD;
+        const int per_e = (per0 + 2 * per1) * g.parts;
+        e = uni(slot / per_e);
+        if (e >= g.E) return;
+        int r = uni(slot - e * per_e), per = per0;
+        if (r >= per0 * g.parts) {
+            r -= per0 * g.parts;
+            per = per1;
+            sel = uni(1 + r / (per1 * g.parts));
+            r = uni(r % (per1 * g.parts));
+            M = lda = g.N;
+            N = ldb = g.M;
+            A0 = sel == 1 ? g.a1 : g.a2;
+            B0 = sel == 1 ? g.b1 : g.b2;
+            out = sel == 1 ? g.out1 : g.out2;
         }
-        const int grp = t / (TR_GM * g.n_nt), gsize = min(TR_GM, g.n_mt - grp * TR_GM);
-        const int rem = t - grp * TR_GM * g.n_nt;
-        m0 = __builtin_amdgcn_readfirstlane((grp * TR_GM + rem % gsize) * BM);
-        n0 = __builtin_amdgcn_readfirstlane(rem / gsize * TR_BN);
-        k_beg = __builtin_amdgcn_readfirstlane(min(max(g.offsets[e], 0), g.n_rows));
-        k_len = max(__builtin_amdgcn_readfirstlane(min(g.offsets[e + 1], g.n_rows)) - k_beg, 0);
-        out += (size_t)e * g.M * g.N;
+        range = uni(r / per);
+        const int t = xcd * per + uni(r % per);
+        if (t >= tiles_of(M, N)) return;
+        const int n_mt = (M + BM - 1) / BM, n_nt = (N + TR_BN - 1) / TR_BN;
+        const int grp = t / (TR_GM * n_nt), gsize = min(TR_GM, n_mt - grp * TR_GM);
+        const int rem = t - grp * TR_GM * n_nt;
+        m0 = uni((grp * TR_GM + rem % gsize) * BM);
+        n0 = uni(rem / gsize * TR_BN);
+        k_beg = uni(min(max(g.offsets[e], 0), g.n_rows));
+        k_len = max(uni(min(g.offsets[e + 1], g.n_rows)) - k_beg, 0);
+        out += (size_t)e * M * N;
         if constexpr (PART) {  // whole stages, but for the last range's end
-            range = __builtin_amdgcn_readfirstlane(res_part % g.parts);
             const int beg = (int)((long long)k_len * range / g.parts) & ~63;
             const int end = range + 1 < g.parts ? (int)((long long)k_len * (range + 1) / g.parts) & ~63 : k_len;
             k_beg += beg;
             k_len = end - beg;
         } else if (k_len == 0) {  // an expert without rows: zeros, by whole lines
             const int c = n0 + (threadIdx.x & 31) * 8;
-            for (int r = m0 + threadIdx.x / 32; r < min(m0 + BM, g.M); r += 8)
-                if (c < g.N) *reinterpret_cast<u32x4*>(out + (size_t)r * g.N + c) = u32x4{0, 0, 0, 0};
+            for (int r = m0 + threadIdx.x / 32; r < min(m0 + BM, M); r += 8)
+                if (c < N) *reinterpret_cast<u32x4*>(out + (size_t)r * N + c) = u32x4{0, 0, 0, 0};
             return;
         }
     } else {
-        const int n_mt = *g.plan.mt_count;
-        const int tiles = n_mt * g.n_nt;
+        const GroupTiles gt(g.plan, g.E, BM, g.offsets);
+        const int tiles = gt.count * g.n_nt;
         const int per = (tiles * (PART ? g.parts : 1) + PF_XCD - 1) / PF_XCD;
         int t = xcd * per + slot;
         if (slot >= per || t >= tiles * (PART ? g.parts : 1)) return;
         if constexpr (PART) {
-            range = __builtin_amdgcn_readfirstlane(t % g.parts);
+            range = uni(t % g.parts);
             t /= g.parts;
         }
-        const PfTile tl = pf_tile(t, n_mt, g.n_nt, g.plan.mt_expert, g.plan.mt_row0, g.offsets, g.n_rows);
-        e = tl.e;
-        row0 = tl.row0;
-        row_end = min(tl.row_end, row0 + BM);
-        n0 = tl.nt * (MODE == TR_GATE ? 128 : TR_BN);
+        const PfTile tl = gt.tile(t, g.n_nt, g.n_rows);
+        e = uni(tl.e);
+        row0 = uni(tl.row0);
+        row_end = min(uni(tl.row_end), row0 + BM);
+        if (row0 >= row_end) return;  // (offsets past the rows)
+        n0 = uni(tl.nt) * (MODE == TR_GATE ? 128 : TR_BN);
         const size_t we = (size_t)e * g.K * g.N;
         B0 += we;
         if (MODE == TR_DX || MODE == TR_GATE) B1 += we;
@@ -182,24 +195,24 @@ void ffn_train_kernel(TrainArgs g) {
     // [k][n] halves: instruction j of wave w fills rows 2 (w + 4 j) and the next
     // ([k][m] with 128 m: four rows from 4 (w + 4 j)); lane p slot p % 32 (16).
     const int brow = 2 * wave + (lane >> 5);
-    uint32_t vb[2] = {(uint32_t)(brow * g.ldb + ((lane & 31) ^ ((brow & 3) << 2)) * 8) * 2, 0};
+    uint32_t vb[2] = {(uint32_t)(brow * ldb + ((lane & 31) ^ ((brow & 3) << 2)) * 8) * 2, 0};
     constexpr int ACH = BM / 8;           // chunks of a [k][m] row
     constexpr int ARI = kWave / ACH;      // rows of one instruction
     uint32_t va[2];
     int ac[2];
     if constexpr (WG) {
         const int arow = ARI * wave + lane / ACH;
-        va[0] = va[1] = (uint32_t)(arow * g.lda + ((lane % ACH) ^ ((arow & 3) << 2)) * 8) * 2;
+        va[0] = va[1] = (uint32_t)(arow * lda + ((lane % ACH) ^ ((arow & 3) << 2)) * 8) * 2;
         ac[0] = ac[1] = 0;
     } else {
-        row_chunks(0, va, ac, g.lda);
+        row_chunks(0, va, ac, lda);
     }
     // [n][k] halves: as [r][k] ones, of 256 weight rows.  TR_GATE: 128 rows of
     // each weight in alternating blocks of 32, so a lane's gate and up sums meet;
     // a wave instruction then fetches rows of one weight: with 64 k a stage, of
     // W1 for even j and W3 for odd, with 32, of W1 in waves 0 and 1.
     int bc[2] = {0, 0};
-    if constexpr (BROWS) row_chunks(MODE == TR_GATE && TR_BK == 32 ? 16 * (wave & 2) : 0, vb, bc, g.ldb);
+    if constexpr (BROWS) row_chunks(MODE == TR_GATE && TR_BK == 32 ? 16 * (wave & 2) : 0, vb, bc, ldb);
     // Descriptors of stage kt: its first element and the bytes from there on that exist.
     auto rsrc = [&](const bf16* p, int bytes) __attribute__((always_inline)) {
         return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000);
@@ -207,23 +220,23 @@ void ffn_train_kernel(TrainArgs g) {
     auto rs_a = [&](int kt) __attribute__((always_inline)) {
         if constexpr (WG) {
             const int v = min(max(k_len - kt * TR_BK, 0), TR_BK);
-            return rsrc(A0 + (size_t)(k_beg + kt * TR_BK) * g.lda + m0, v > 0 ? (v * g.lda - m0) * 2 : 0);
+            return rsrc(A0 + (size_t)(k_beg + kt * TR_BK) * lda + m0, v > 0 ? (v * lda - m0) * 2 : 0);
         } else {
             const int seg = MODE == TR_DX && kt >= nk1;
             const int k0 = (kt - (seg ? nk1 : 0)) * TR_BK;
-            const int bytes = kt < ke ? ((row_end - row0) * g.lda - k0) * 2 : 0;
-            return rsrc((seg ? A1 : A0) + (size_t)row0 * g.lda + k0, bytes);
+            const int bytes = kt < ke ? ((row_end - row0) * lda - k0) * 2 : 0;
+            return rsrc((seg ? A1 : A0) + (size_t)row0 * lda + k0, bytes);
         }
     };
     auto rs_b = [&](int kt, int which = 0) __attribute__((always_inline)) {
         if constexpr (BROWS) {
-            const int bytes = kt < ke ? (min(g.N - n0, MODE == TR_GATE ? 128 : TR_BN) * g.ldb - kt * TR_BK) * 2 : 0;
-            return rsrc((which ? B1 : B0) + (size_t)n0 * g.ldb + kt * TR_BK, bytes);
+            const int bytes = kt < ke ? (min(N - n0, MODE == TR_GATE ? 128 : TR_BN) * ldb - kt * TR_BK) * 2 : 0;
+            return rsrc((which ? B1 : B0) + (size_t)n0 * ldb + kt * TR_BK, bytes);
         }
         const int seg = MODE == TR_DX && kt >= nk1;
         const int k0 = (kt - (seg ? nk1 : 0)) * TR_BK;
         const int v = kt < ke ? min(k_len - k0, TR_BK) : 0;
-        return rsrc((seg ? B1 : B0) + (size_t)(k_beg + k0) * g.ldb + n0, v > 0 ? (v * g.ldb - n0) * 2 : 0);
+        return rsrc((seg ? B1 : B0) + (size_t)(k_beg + k0) * ldb + n0, v > 0 ? (v * ldb - n0) * 2 : 0);
     };
     auto ld_a = [&](__amdgpu_buffer_rsrc_t r, int kt, int j, bf16* dst) __attribute__((always_inline)) {
         uint32_t v = va[j & 1];
@@ -233,7 +246,7 @@ void ffn_train_kernel(TrainArgs g) {
         }
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             r, (__attribute__((address_space(3))) void*)(dst + (wave + 4 * j) * 512), 16, v,
-            WG ? j * (4 * ARI * 2) * g.lda : j * (4096 / TR_BK) * g.lda, 0, 0);
+            WG ? j * (4 * ARI * 2) * lda : j * (4096 / TR_BK) * lda, 0, 0);
     };
     auto ld_b = [&](const __amdgpu_buffer_rsrc_t (&r)[2], int kt, int j, bf16* dst) __attribute__((always_inline)) {
         uint32_t v = vb[BROWS ? j & 1 : 0];
@@ -243,7 +256,7 @@ void ffn_train_kernel(TrainArgs g) {
         const int rows = MODE == TR_GATE && TR_BK == 64 ? (j >> 1) * JR : j * JR;
         const int which = MODE != TR_GATE ? 0 : TR_BK == 64 ? j & 1 : 0;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            r[which], (__attribute__((address_space(3))) void*)(dst + (wave + 4 * j) * 512), 16, v, rows * 2 * g.ldb, 0, 0);
+            r[which], (__attribute__((address_space(3))) void*)(dst + (wave + 4 * j) * 512), 16, v, rows * 2 * ldb, 0, 0);
     };
     // The weights' descriptors of stage kt (TR_GATE with 32 k a stage: each wave's own weight).
     struct RsB {
@@ -473,9 +486,9 @@ void ffn_train_kernel(TrainArgs g) {
         // fp32 sums, 32 rows x 64 columns (8 KB) at a time
         float* const sf = reinterpret_cast<float*>(st);
         // of the range: result e * sels + (which of them), or all rows
-        float* const dst = WG ? g.part + (((size_t)range * g.E + e) * g.sels + (out_sel ? 1 : 0)) * g.M * g.N
-                              : g.part + (size_t)range * g.n_rows * g.N;
-        const int r0 = WG ? m0 : row0, r_end = WG ? g.M : row_end;
+        float* const dst = WG ? g.part + (((size_t)range * g.E + e) * 3 + sel) * M * N
+                              : g.part + (size_t)range * g.n_rows * N;
+        const int r0 = WG ? m0 : row0, r_end = WG ? M : row_end;
         const int lrow = el >> 4, lch = el & 15;
 #pragma unroll
         for (int p = 0; p < 2 * NTB; ++p) {
@@ -494,7 +507,7 @@ void ffn_train_kernel(TrainArgs g) {
             for (int i = 0; i < 8; ++i) {
                 const int rl = i * 4 + lrow, r = r0 + mrow + mb * 32 + rl;
                 const f32x4 v = *reinterpret_cast<const f32x4*>(sf + rl * 64 + ((lch ^ (rl & 15)) << 2));
-                if (r < r_end && c < g.N) *reinterpret_cast<f32x4*>(dst + (size_t)r * g.N + c) = v;
+                if (r < r_end && c < N) *reinterpret_cast<f32x4*>(dst + (size_t)r * N + c) = v;
             }
         }
     } else if constexpr (MODE == TR_DACT) {
@@ -503,12 +516,12 @@ void ffn_train_kernel(TrainArgs g) {
         const int lrow = el >> 3, lch = el & 7;  // eight chunks of eight columns per row
         bf16x8 gv[2][4], uv[2][4];  // a pass's gate and up, loaded one pass ahead
         auto fetch = [&](int p) __attribute__((always_inline)) {
-            const int c = min(ncol + (p & 1) * 64 + lch * 8, g.N - 8);
+            const int c = min(ncol + (p & 1) * 64 + lch * 8, N - 8);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = min(row0 + mrow + (p >> 1) * 32 + i * 8 + lrow, row_end - 1);
-                gv[p & 1][i] = *reinterpret_cast<const bf16x8*>(g.gate + (size_t)r * g.N + c);
-                uv[p & 1][i] = *reinterpret_cast<const bf16x8*>(g.up + (size_t)r * g.N + c);
+                gv[p & 1][i] = *reinterpret_cast<const bf16x8*>(g.gate + (size_t)r * N + c);
+                uv[p & 1][i] = *reinterpret_cast<const bf16x8*>(g.up + (size_t)r * N + c);
             }
         };
         fetch(0);
@@ -540,8 +553,8 @@ void ffn_train_kernel(TrainArgs g) {
                     o1[j] = (bf16)v.du;
                     o2[j] = (bf16)v.act;
                 }
-                if (r < row_end && c < g.N) {
-                    const size_t at = (size_t)r * g.N + c;
+                if (r < row_end && c < N) {
+                    const size_t at = (size_t)r * N + c;
                     *reinterpret_cast<bf16x8*>(g.out0 + at) = o0;
                     *reinterpret_cast<bf16x8*>(g.out1 + at) = o1;
                     *reinterpret_cast<bf16x8*>(g.out2 + at) = o2;
@@ -576,14 +589,14 @@ void ffn_train_kernel(TrainArgs g) {
             for (int i = 0; i < NTB * 4; ++i) {
                 const int rl = i * 8 + lrow, r = row0 + mrow + rl;
                 const bf16x8 v = *reinterpret_cast<const bf16x8*>(st + rl * 64 + ((lch ^ (rl & 7)) << 3));
-                if (r < row_end && c < g.N) *reinterpret_cast<bf16x8*>(dst + (size_t)r * g.N + c) = v;
+                if (r < row_end && c < N) *reinterpret_cast<bf16x8*>(dst + (size_t)r * N + c) = v;
             }
         }
     } else {
         // in passes of the rows that a unit holds
         constexpr int PB = RING5 ? NTB : 1;  // 32-row blocks per pass
         const int lrow = el >> 4, lch = el & 15;  // 16 chunks of eight columns per row
-        const int r_end = WG ? g.M : row_end, r0 = (WG ? m0 : row0) + mrow;
+        const int r_end = WG ? M : row_end, r0 = (WG ? m0 : row0) + mrow;
         const int c = ncol + lch * 8;
 #pragma unroll
         for (int p = 0; p < NTB; p += PB) {
@@ -604,7 +617,7 @@ void ffn_train_kernel(TrainArgs g) {
             for (int i = 0; i < PB * 8; ++i) {
                 const int rl = i * 4 + lrow, r = r0 + p * 32 + rl;
                 const bf16x8 v = *reinterpret_cast<const bf16x8*>(st + rl * 128 + ((lch ^ (rl & 7)) << 3));
-                if (r < r_end && c < g.N) *reinterpret_cast<bf16x8*>(out + (size_t)r * g.N + c) = v;
+                if (r < r_end && c < N) *reinterpret_cast<bf16x8*>(out + (size_t)r * N + c) = v;
             }
         }
     }
@@ -617,12 +630,13 @@ hipError_t launch_tiles(const TrainArgs& g, int bm, unsigned grid, hipStream_t s
     return hipGetLastError();
 }
 
-// Adds the ranges of rows in order; result blockIdx.y of E * sels.
-__global__ __launch_bounds__(256) void dw_reduce_kernel(size_t n, int parts, int sels, const float* __restrict__ part,
-                                                       bf16* __restrict__ out0, bf16* __restrict__ out1) {
-    const int res = blockIdx.y;
+// Adds the ranges of rows in order; result blockIdx.y of 3 E.
+__global__ __launch_bounds__(256) void dw_reduce_kernel(size_t n, int parts, const float* __restrict__ part,
+                                                       bf16* __restrict__ out0, bf16* __restrict__ out1,
+                                                       bf16* __restrict__ out2) {
+    const int res = blockIdx.y, sel = res % 3;
     const float* src = part + (size_t)res * n;
-    bf16* dst = (res % sels ? out1 : out0) + (size_t)(res / sels) * n;
+    bf16* dst = (sel == 0 ? out0 : sel == 1 ? out1 : out2) + (size_t)(res / 3) * n;
     const size_t step = (size_t)gridDim.y * n;
     for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (size_t)gridDim.x * 1024) {
         f32x4 v = *reinterpret_cast<const f32x4*>(src + i);
@@ -655,46 +669,56 @@ size_t row_part_bytes(int n, int E, int N, int K) {
     return parts > 1 ? (size_t)parts * n * N * sizeof(float) : 0;
 }
 
-// Ranges that the rows of TR_DW are cut into: with few result tiles and long
-// groups, enough for two workgroups per compute unit, 512 rows or more each.
-int dw_ranges(int n, int E, int M, int N, int sels) {
-    const long tiles = (long)((M + 127) / 128) * ((N + TR_BN - 1) / TR_BN) * E * sels;
-    return (int)std::max(1L, std::min(512 / tiles, (long)n / E / 512));
-}
-size_t dw_part_bytes(int n, int E, int M, int N, int sels) {
-    const int parts = dw_ranges(n, E, M, N, sels);
-    return parts > 1 ? (size_t)parts * E * sels * M * N * sizeof(float) : 0;
+// Slots of one expert's results per XCD (TR_DW).
+long dw_slots(int d, int F, int bm) {
+    const auto per = [&](int m, int n) {
+        return ((long)((m + bm - 1) / bm) * ((n + TR_BN - 1) / TR_BN) + PF_XCD - 1) / PF_XCD;
+    };
+    return per(d, F) + 2 * per(F, d);
 }
 
-// The result of P^T Q for every expert (and for a second P where p1 is given).
-hipError_t launch_dw(int n, int E, int M, int N, const bf16* p0, const bf16* p1, const bf16* q, bf16* out0, bf16* out1,
-                     const int32_t* offsets, float* part, hipStream_t s) {
+// Ranges that the rows of TR_DW are cut into: with few result tiles and long
+// groups, enough for two workgroups per compute unit, 512 rows or more each
+// (one expert of 6244 rows, d 520, F 152: the backward pass 242 -> 75 us).
+int dw_ranges(int n, int E, int d, int F) {
+    const long tiles = ((long)((d + 127) / 128) * ((F + TR_BN - 1) / TR_BN) +
+                        2L * ((F + 127) / 128) * ((d + TR_BN - 1) / TR_BN)) * E;
+    return (int)std::max(1L, std::min(512 / tiles, (long)n / E / 512));
+}
+size_t dw_part_bytes(int n, int E, int d, int F) {
+    const int parts = dw_ranges(n, E, d, F);
+    return parts > 1 ? (size_t)parts * 3 * E * d * F * sizeof(float) : 0;
+}
+
+// dW2 = dh^T act, dW1 = dgate^T x and dW3 = dup^T x of every expert, in one launch.
+hipError_t launch_dw(int n, int E, int d, int F, const bf16* dh, const bf16* act, const bf16* dgate, const bf16* dup,
+                     const bf16* x, bf16* dw2, bf16* dw1, bf16* dw3, const int32_t* offsets, float* part,
+                     hipStream_t s) {
     TrainArgs g{};
-    g.a0 = p0;
-    g.a1 = p1;
-    g.b0 = q;
-    g.out0 = out0;
-    g.out1 = out1;
+    g.a0 = dh;
+    g.b0 = act;
+    g.out0 = dw2;
+    g.a1 = dgate;
+    g.a2 = dup;
+    g.b1 = g.b2 = x;
+    g.out1 = dw1;
+    g.out2 = dw3;
     g.n_rows = n;
     g.E = E;
-    g.M = g.lda = M;
-    g.N = g.ldb = N;
-    g.sels = p1 != nullptr ? 2 : 1;
+    g.M = g.lda = d;
+    g.N = g.ldb = F;
     g.offsets = offsets;
-    g.parts = dw_ranges(n, E, M, N, g.sels);
+    g.parts = dw_ranges(n, E, d, F);
     g.part = part;
     const int bm = g.parts == 1 && n >= TR_DW_LONG * E ? 256 : 128;
-    g.n_mt = (M + bm - 1) / bm;
-    g.n_nt = (N + TR_BN - 1) / TR_BN;
-    const long per = ((long)g.n_mt * g.n_nt + PF_XCD - 1) / PF_XCD;
-    const unsigned grid = (unsigned)(per * E * g.sels * g.parts * PF_XCD);
+    const unsigned grid = (unsigned)(dw_slots(d, F, bm) * E * g.parts * PF_XCD);
     if (g.parts == 1) return launch_tiles<TR_DW, false>(g, bm, grid, s);
     ffn_train_kernel<TR_DW, 128, false, true><<<grid, 256, 0, s>>>(g);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const size_t each = (size_t)M * N;
-    dw_reduce_kernel<<<dim3((unsigned)std::min<size_t>((each + 1023) / 1024, 1024), E * g.sels), 256, 0, s>>>(
-        each, g.parts, g.sels, part, out0, out1);
+    const size_t each = (size_t)d * F;
+    dw_reduce_kernel<<<dim3((unsigned)std::min<size_t>((each + 1023) / 1024, 1024), 3 * E), 256, 0, s>>>(
+        each, g.parts, part, dw2, dw1, dw3);
     return hipGetLastError();
 }
 
@@ -738,7 +762,8 @@ hipError_t launch_ffn_train_tiles(int n, int E, int d, int F, const bf16* x, con
                                   hipStream_t s) {
     const int bm = train_bm(n, E, std::min(d, F));
     TrainArgs g{};
-    hipError_t err = launch_row_plan(n, E, bm, offsets, ws, &g.plan, s);
+    hipError_t err = hipSuccess;
+    if (E > GroupTiles::kMax) err = launch_row_plan(n, E, bm, offsets, ws, &g.plan, s);
     if (err != hipSuccess) return err;
     g.n_rows = n;
     g.E = E;
@@ -765,8 +790,7 @@ hipError_t launch_ffn_train_tiles(int n, int E, int d, int F, const bf16* x, con
 
 // The row plan, then the ranges' sums of one product after the other.
 size_t ffn_grad_ws_bytes(int n, int E, int d, int F) {
-    return row_plan_bytes(n, E) + std::max(std::max(dw_part_bytes(n, E, d, F, 1), dw_part_bytes(n, E, F, d, 2)),
-                                           row_part_bytes(n, E, d, 2 * F));
+    return row_plan_bytes(n, E) + std::max(dw_part_bytes(n, E, d, F), row_part_bytes(n, E, d, 2 * F));
 }
 
 hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int32_t* offsets, const bf16* w1,
@@ -775,7 +799,8 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
                            hipStream_t s) {
     const int bm = train_bm(n, E, std::min(d, F));
     RowPlan plan;
-    hipError_t err = launch_row_plan(n, E, bm, offsets, ws, &plan, s);
+    hipError_t err = hipSuccess;
+    if (E > GroupTiles::kMax) err = launch_row_plan(n, E, bm, offsets, ws, &plan, s);
     if (err != hipSuccess) return err;
     float* part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + row_plan_bytes(n, E));
     auto grid = [&](int n_nt) { return train_grid(n, E, bm, n_nt); };
@@ -798,8 +823,8 @@ hipError_t launch_ffn_grad(int n, int E, int d, int F, const bf16* x, const int3
                          : launch_tiles<TR_DACT, true>(g, bm, grid(g.n_nt), s);
     if (err != hipSuccess) return err;
     if (dw2 != nullptr) {
-        if ((err = launch_dw(n, E, d, F, dh, nullptr, act, dw2, nullptr, offsets, part, s)) != hipSuccess) return err;
-        if ((err = launch_dw(n, E, F, d, dgate, dup, x, dw1, dw3, offsets, part, s)) != hipSuccess) return err;
+        err = launch_dw(n, E, d, F, dh, act, dgate, dup, x, dw2, dw1, dw3, offsets, part, s);
+        if (err != hipSuccess) return err;
     }
     if (dx != nullptr) {
         g.a0 = dgate;

@@ -39,8 +39,8 @@ struct GemmArgs {
     int M, N, K;      // GM_TN: C is [M][N]; else K is the reduction length
     int n_rows;       // grouped rows
     int E;            // experts (GM_TN: the grid's z counts them, once or twice)
-    RowPlan plan;     // row tiles of the groups (mt_count NULL: one group of n_rows rows)
-    const int32_t* offsets;  // NULL: one group; GM_TN then cuts its rows into gridDim.z parts
+    RowPlan plan;     // row tiles of the groups (mt_count NULL: up to 64 experts, see GroupTiles)
+    const int32_t* offsets;  // NULL: one group of n_rows rows; GM_TN then cuts it into gridDim.z parts
 };
 
 // Eight consecutive elements of a row as floats; zeros past `left` elements.
@@ -102,10 +102,10 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi e
             k_beg = (int)((long long)g.n_rows * e / gridDim.z);
             k_end = (int)((long long)g.n_rows * (e + 1) / gridDim.z);
         }
-    } else if (g.plan.mt_count != nullptr) {
-        if ((int)blockIdx.x >= *g.plan.mt_count) return;
-        e = g.plan.mt_expert[blockIdx.x] & 0x7FF;
-        m0 = g.plan.mt_row0[blockIdx.x];
+    } else if (g.offsets != nullptr) {
+        const GroupTiles gt(g.plan, g.E, GM_T, g.offsets);
+        if ((int)blockIdx.x >= gt.count) return;
+        gt.rows(blockIdx.x, e, m0);
         m_end = min(g.offsets[e + 1], g.n_rows);
     } else {
         m0 = blockIdx.x * GM_T;
