@@ -7,10 +7,12 @@
 //   GM_NN  C[r][n] = sum_k A[r][k] B[k][n]
 //   GM_TN  C[m][n] = sum_r A[r][m] B[r][n]     the sum runs over the group's rows
 //
-// A workgroup of four waves (2 x 2) owns a tile of 128, or of 64 where tiles of
-// 128 would leave compute units idle: the MFMAs of a 128-wide tile take 14 us
-// per 128 of k and product pair, whatever its rows hold (64 rows over 8 experts,
-// d 128, F 256: 21 us a product with tiles of 128).
+// A workgroup of four waves (2 x 2) owns a tile of 64, of which more fit on a
+// compute unit and hide each other's loads, or of 128, with half the LDS reads
+// per MFMA, once there are many.  A tile of 32 is for few: each wave multiplies
+// all of it over its own quarter of a step's k, and the four sums are joined in
+// order at the end, so the chain of MFMAs is a quarter as long and four times
+// as many workgroups run.
 // Operands go through registers (the next k step is loaded while the present
 // one is multiplied) into LDS tiles [k][row], padded so that the
 // column reads of the MFMA operands and the transposing writes fall in
@@ -23,8 +25,11 @@
 namespace moe {
 
 constexpr int GM_K = 32;  // k per step
-// The tile for a launch of `tiles` tiles of 128.
-inline int gm_tile(long tiles) { return tiles < 512 ? 64 : 128; }
+// The tile for a launch of `tiles` tiles of 128 (FFN backward, 16384 rows, 8
+// experts: d 1024, F 2048, 512 to 1024 tiles a product: 3.84 ms with 64, 4.00
+// with 128 where the sum is over k, 3.68 where it is over rows; d 2048, F 4096,
+// 2048 tiles: 15.38, 14.75 and 14.74 ms).
+inline int gm_tile(long tiles) { return tiles < 1536 ? 64 : 128; }
 enum { GM_NT, GM_NN, GM_TN };
 
 // One product of every group.  a[1], b[1]: the second factor pair where the
@@ -78,11 +83,18 @@ __device__ __forceinline__ void gm_load8(float (&r)[8], const T* p, int left) {
 template <int GM_T, int LAYOUT, bool DUAL, int SEGS, bool VA, bool VB, typename TA, typename TB, typename Epi>
 __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi epi) {
     constexpr int NB = DUAL ? 2 : 1;
-    constexpr int GM_LD = GM_T + 4;             // padded LDS row (floats)
-    constexpr int GM_H = GM_T * GM_K / 8 / 256;  // 8-element vectors per thread and operand
-    constexpr int BL = GM_T / 64;               // 32 x 32 blocks per wave and side
-    __shared__ __align__(16) float sA[GM_K][GM_LD];
-    __shared__ __align__(16) float sB[NB][GM_K][GM_LD];
+    constexpr bool KSPLIT = GM_T == 32;          // each wave the whole tile, over a quarter of a step's k
+    constexpr int SK = KSPLIT ? 4 * GM_K : GM_K;  // k per step
+    // padded LDS rows (floats); a tile of 32 that is written column by column
+    // takes an odd row, else the writes of all k would share a bank
+    constexpr int LA = KSPLIT && LAYOUT != GM_TN ? 33 : GM_T + 4;
+    constexpr int LB = KSPLIT && LAYOUT == GM_NT ? 33 : GM_T + 4;
+    constexpr int GM_H = GM_T * SK / 8 / 256;    // 8-element vectors per thread and operand
+    constexpr int BL = KSPLIT ? 1 : GM_T / 64;   // 32 x 32 blocks per wave and side
+    static_assert(!KSPLIT || 4 * GM_T * GM_T * NB <= SK * (LA + NB * LB), "the waves' sums fit the operands' LDS");
+    __shared__ __align__(16) float lds[SK * (LA + NB * LB)];
+    float(*const sA)[LA] = reinterpret_cast<float(*)[LA]>(lds);
+    float(*const sB)[LB] = reinterpret_cast<float(*)[LB]>(lds + SK * LA);  // product i: rows SK i on
     const int tid = threadIdx.x;
     const int lane = lane_id();
     const int wave = tid / kWave;
@@ -113,7 +125,7 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi e
     }
 
     // a [rows][k] tile: row (and every KR on) and first k of this thread
-    constexpr int KT = GM_K / 8, KR = 256 / KT;
+    constexpr int KT = SK / 8, KR = 256 / KT;
     const int kr = tid / KT, kc = (tid % KT) * 8;
     // a [k][columns] tile: k (and every SR on) and first column
     constexpr int ST = GM_T / 8, SR = 256 / ST;
@@ -146,13 +158,13 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi e
             }
         }
     };
-    auto store_rows = [&](float (&s)[GM_K][GM_LD], const float (&r)[GM_H][8]) {
+    auto store_rows = [&](auto s, const float (&r)[GM_H][8]) {
 #pragma unroll
         for (int h = 0; h < GM_H; ++h)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[kc + j][kr + KR * h] = r[h][j];
     };
-    auto store_cols = [&](float (&s)[GM_K][GM_LD], const float (&r)[GM_H][8]) {
+    auto store_cols = [&](auto s, const float (&r)[GM_H][8]) {
 #pragma unroll
         for (int h = 0; h < GM_H; ++h) {
             *reinterpret_cast<f32x4*>(&s[sr + SR * h][sc]) = f32x4{r[h][0], r[h][1], r[h][2], r[h][3]};
@@ -160,7 +172,8 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi e
         }
     };
 
-    const int wm = (wave & 1) * (GM_T / 2), wn = (wave >> 1) * (GM_T / 2);
+    const int wm = KSPLIT ? 0 : (wave & 1) * (GM_T / 2), wn = KSPLIT ? 0 : (wave >> 1) * (GM_T / 2);
+    const int wk = KSPLIT ? wave * GM_K : 0;
     const int fr = lane & 31, fk = lane >> 5;
     f32x16 acc[NB][BL][BL];
 #pragma unroll
@@ -172,7 +185,7 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi e
 #pragma unroll
                 for (int q = 0; q < 16; ++q) acc[i][a][b][q] = 0.0f;
 
-    const int per = (k_end - k_beg + GM_K - 1) / GM_K;  // steps of one segment
+    const int per = (k_end - k_beg + SK - 1) / SK;  // steps of one segment
     const int steps = per * SEGS;
     if (steps > 0) load(0, k_beg);
     for (int st = 0; st < steps; ++st) {
@@ -181,24 +194,24 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi e
         else store_rows(sA, ra);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            if constexpr (LAYOUT == GM_NT) store_rows(sB[i], rb[i]);
-            else store_cols(sB[i], rb[i]);
+            if constexpr (LAYOUT == GM_NT) store_rows(sB + SK * i, rb[i]);
+            else store_cols(sB + SK * i, rb[i]);
         }
         __syncthreads();
         if (st + 1 < steps) {
             const int seg = SEGS > 1 && st + 1 >= per ? 1 : 0;
-            load(seg, k_beg + (st + 1 - seg * per) * GM_K);
+            load(seg, k_beg + (st + 1 - seg * per) * SK);
         }
 #pragma unroll
         for (int k = 0; k < GM_K; k += 2) {
             float a[BL];
 #pragma unroll
-            for (int mb = 0; mb < BL; ++mb) a[mb] = sA[k + fk][wm + mb * 32 + fr];
+            for (int mb = 0; mb < BL; ++mb) a[mb] = sA[wk + k + fk][wm + mb * 32 + fr];
 #pragma unroll
             for (int i = 0; i < NB; ++i)
 #pragma unroll
                 for (int nb = 0; nb < BL; ++nb) {
-                    const float b = sB[i][k + fk][wn + nb * 32 + fr];
+                    const float b = sB[SK * i + wk + k + fk][wn + nb * 32 + fr];
 #pragma unroll
                     for (int mb = 0; mb < BL; ++mb)
                         acc[i][nb][mb] = __builtin_amdgcn_mfma_f32_32x32x2f32(b, a[mb], acc[i][nb][mb], 0, 0, 0);
@@ -206,6 +219,33 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs<TA, TB> g, Epi e
         }
     }
     // element i of block (nb, mb): column 8 (i / 4) + 4 (lane / 32) + i % 4, row lane % 32
+    if constexpr (KSPLIT) {  // wave q joins the four sums of elements 4 q .. 4 q + 3 and hands them on
+        f32x4* const sum = reinterpret_cast<f32x4*>(lds);  // [product][wave][q][lane]
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                sum[((i * 4 + wave) * 4 + q) * kWave + lane] = f32x4{acc[i][0][0][4 * q], acc[i][0][0][4 * q + 1], acc[i][0][0][4 * q + 2],
+                                              acc[i][0][0][4 * q + 3]};
+        __syncthreads();
+        const int m = m0 + fr, n = n0 + 8 * wave + 4 * fk;
+        if (m >= m_end || n >= g.N) return;
+        f32x4 v[2];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            f32x4 t = sum[(i * 16 + wave) * kWave + lane];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+                const f32x4 u = sum[((i * 4 + w) * 4 + wave) * kWave + lane];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) t[j] += u[j];
+            }
+            v[i] = t;
+        }
+        epi(e, sel, m, n, g.N, v);
+        return;
+    }
 #pragma unroll
     for (int mb = 0; mb < BL; ++mb) {
         const int m = m0 + wm + mb * 32 + fr;

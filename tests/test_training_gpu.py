@@ -65,6 +65,8 @@ FFN_CASES = [
     (64, 2, 264, 200, [33, 31, 64, 0]),
     (3000, 1, 136, 72, [3000]),  # few weight tiles, long groups: rows summed in ranges
     (2200, 2, 64, 320, [2500, 1, 0]),
+    (2000, 1, 520, 512, [700, 0, 1233]),  # fp32: enough tiles for those of 64
+    (49152, 1, 520, 512, [1019 + (e * 37) % 11 for e in range(47)] + [130]),  # and of 128 (backward)
 ]
 
 
