@@ -27,13 +27,16 @@
 // past an operand's last element is ever read.
 //
 // Bounds.  Long groups: the matrix pipes, at the clock that power allows
-// (16384 rows, 8 experts, d 4096, F 14336: da 1.76 ms, dW2 1.50, dW1 and dW3
-// 3.05, dx 3.28, together 9.5 ms, 1210 TFLOP/s, what a large library product
-// reaches).  Short groups: the weights' bytes (4096 rows, 32 experts, d 7168, F
-// 2048: da 187 us and dx 445 us at 5.0 and 4.2 TB/s; dW2 265 us and dW1, dW3
-// 570 us, 3.4 TB/s of writes: with one stage of rows the same tiles are written
-// at 6 TB/s, so what is left there is the operands' way into the LDS, which the
-// stores of the other workgroup of the CU hide only in part).
+// (16384 rows, 8 experts, d 4096, F 14336: da 1.77 ms, the three weight gradients
+// 4.58, dx 3.30, together 9.65 ms, 1196 TFLOP/s; a large library product reaches
+// 1210).  Short groups: the weights' bytes (4096 rows, 32 experts, d 7168, F
+// 2048: da 187 us and dx 450 us at 5.0 and 4.2 TB/s; the weight gradients 833
+// us, 3.4 TB/s of writes: with one stage of rows the same tiles are written at 6
+// TB/s, so what is left there is the operands' way into the LDS, which the
+// stores of the other workgroup of the CU hide only in part).  The weight
+// gradients share a launch, and row tiles of up to 64 experts are found without
+// a plan launch, for small layers (333 tokens, 5 experts, K 3, d 264, F 200: 45
+// -> 34 us; the large ones above stay within the noise).
 #include <algorithm>
 #include <type_traits>
 
@@ -50,7 +53,7 @@ enum { TR_DACT, TR_DX, TR_DW, TR_GATE, TR_DOWN };
 constexpr int TR_BN = 256;
 // Rows per expert from which TR_DW takes 256 x 256 tiles, one workgroup per CU;
 // shorter groups take 128 x 256, two per CU, since a tile's loads and its stores
-// then overlap (128 rows per expert: 634 -> 570 us for dW1 and dW3 above).
+// then overlap (dW1 and dW3 of the 128 rows per expert above: 634 -> 570 us).
 constexpr int TR_DW_LONG = 512;
 constexpr int TR_GM = 8;  // row tiles per group in TR_DW's order
 
@@ -397,8 +400,9 @@ void ffn_train_kernel(TrainArgs g) {
         __builtin_amdgcn_sched_barrier(0);
     };
     // Stage kt + 2 into slot (kt + 2) % 3, half of its loads in each of the
-    // stage's two 16-wide parts.
-    auto step3 = [&](int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA, bf16* pB) __attribute__((always_inline)) {
+    // stage's two 16-wide parts (L; the first stage's step finds them on the way).
+    auto step3 = [&](auto l_c, int kt, bf16* cA, bf16* cB, const bf16* nA, const bf16* nB, bf16* pA, bf16* pB) __attribute__((always_inline)) {
+        constexpr bool L = decltype(l_c)::value;
         constexpr int V = NLD / 2;
         const auto ra = rs_a(ks + kt + 2);
         const RsB rb = rs_bs(ks + kt + 2);
@@ -410,18 +414,18 @@ void ffn_train_kernel(TrainArgs g) {
             }
         };
         read(cA, cB, 1, fb);
-        lds(0);
+        if constexpr (L) lds(0);
         mma(fa);
-        weave(std::integral_constant<int, V>{});
+        weave(std::integral_constant<int, L ? V : 0>{});
         __builtin_amdgcn_sched_barrier(0);
         PF_WAIT_LGKM0();
-        PF_WAIT_VM(V);
+        PF_WAIT_VM(L ? V : NLD);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        lds(V);
+        if constexpr (L) lds(V);
         read(nA, nB, 0, fa);
         mma(fb);
-        weave(std::integral_constant<int, V>{});
+        weave(std::integral_constant<int, L ? V : 0>{});
         __builtin_amdgcn_sched_barrier(0);
     };
     auto first = [&](int kt, bf16* dA, bf16* dB) __attribute__((always_inline)) {
@@ -454,19 +458,22 @@ void ffn_train_kernel(TrainArgs g) {
             if (rem > 2) step5(main + 2, u4, u0, u1, u2, u3);
             if (rem > 3) step5(main + 3, u1, u2, u3, u4, u0);
         } else {
+            constexpr std::true_type L{};
             first(0, sA0, sB0);
             first(1, sA1, sB1);
-            PF_WAIT_VM(NLD);
+            first(2, sA2, sB2);
+            PF_WAIT_VM(2 * NLD);
             __builtin_amdgcn_s_barrier();
             read(sA0, sB0, 0, fa);
-            const int main = nk - nk % 3;
-            for (int k = 0; k < main; k += 3) {
-                step3(k, sA0, sB0, sA1, sB1, sA2, sB2);
-                step3(k + 1, sA1, sB1, sA2, sB2, sA0, sB0);
-                step3(k + 2, sA2, sB2, sA0, sB0, sA1, sB1);
+            step3(std::false_type{}, 0, sA0, sB0, sA1, sB1, nullptr, nullptr);
+            const int rem = (nk - 1) % 3, main = nk - rem;
+            for (int k = 1; k < main; k += 3) {
+                step3(L, k, sA1, sB1, sA2, sB2, sA0, sB0);
+                step3(L, k + 1, sA2, sB2, sA0, sB0, sA1, sB1);
+                step3(L, k + 2, sA0, sB0, sA1, sB1, sA2, sB2);
             }
-            if (nk - main > 0) step3(main, sA0, sB0, sA1, sB1, sA2, sB2);
-            if (nk - main > 1) step3(main + 1, sA1, sB1, sA2, sB2, sA0, sB0);
+            if (rem > 0) step3(L, main, sA1, sB1, sA2, sB2, sA0, sB0);
+            if (rem > 1) step3(L, main + 1, sA2, sB2, sA0, sB0, sA1, sB1);
         }
     }
     PF_WAIT_VM(0);
