@@ -887,7 +887,11 @@ void ffn_prefill_kernel(
             const int rl = i * RPI + lrow;
             const int grow = row0 + trow0 + rl;
             const bf16x8 val = *reinterpret_cast<const bf16x8*>(st + rl * W + ((lch ^ (rl & SWM)) << 3));
-            if (grow < row_end && gcol < N) *reinterpret_cast<bf16x8*>(dst + (size_t)grow * N + gcol) = val;
+            if (grow < row_end && gcol < N) {
+                bf16x8* const q = reinterpret_cast<bf16x8*>(dst + (size_t)grow * N + gcol);
+                if constexpr (WHICH == 0) *q = val;
+                else __builtin_nontemporal_store(val, q);  // not read again before the backward pass
+            }
         }
     };
     auto store = [&](auto wbn_c, auto tbn_c) __attribute__((always_inline)) {

@@ -257,7 +257,10 @@ __global__ __launch_bounds__(256) void route_dx_kernel(int T, int d, int E, int 
             const int r = k < K ? slots[k] : -1;
             const bool in = (unsigned)r < (unsigned)n;
             own[i & 1] |= in ? 1u << k : 0u;
-            raw[i & 1][k] = load16(rows + (size_t)(in ? r : 0) * d + cc);  // (row 0 is never added then)
+            // not read again: past the caches, which keep the score gradients (4096
+            // tokens, 256 experts: 220 -> 210 us for the backward pass)
+            const bf16* p = rows + (size_t)(in ? r : 0) * d + cc;  // (row 0 is never added then)
+            raw[i & 1][k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
         }
     };
     float sum[RX_T / 16][8];
