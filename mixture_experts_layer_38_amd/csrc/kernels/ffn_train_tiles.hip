@@ -28,10 +28,10 @@
 //
 // Bounds.  Long groups: the matrix pipes, at the clock that power allows
 // (16384 rows, 8 experts, d 4096, F 14336: da 1.77 ms, the three weight gradients
-// 4.58, dx 3.30, together 9.65 ms, 1196 TFLOP/s; a large library product reaches
+// 4.54, dx 3.28, together 9.6 ms, 1200 TFLOP/s; a large library product reaches
 // 1210).  Short groups: the weights' bytes (4096 rows, 32 experts, d 7168, F
-// 2048: da 187 us and dx 450 us at 5.0 and 4.2 TB/s; the weight gradients 833
-// us, 3.4 TB/s of writes: with one stage of rows the same tiles are written at 6
+// 2048: da 187 us and dx 437 us at 5.0 and 4.3 TB/s; the weight gradients 770 to
+// 850 us, 3.5 TB/s of writes: with one stage of rows the same tiles are written at 6
 // TB/s, so what is left there is the operands' way into the LDS, which the
 // stores of the other workgroup of the CU hide only in part).  The weight
 // gradients share a launch, and row tiles of up to 64 experts are found without
