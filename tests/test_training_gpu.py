@@ -224,6 +224,7 @@ ROUTE_CASES = [
     (64, 1000, 32, 136, "bf16", 0, -1, True, 0.01, 0.001),
     (100, 8, 2, 256, "bf16", 2, -1, False, 0.01, 0.001),
     (2000, 16, 2, 192, "bf16", 3, 40, True, 0.5, 0.1),
+    (6200, 5, 2, 4104, "f32", 0, -1, True, 0.01, 0.001),  # enough tiles for those of 128
 ]
 
 
